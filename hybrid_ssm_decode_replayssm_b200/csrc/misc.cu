@@ -1,5 +1,5 @@
 // Read-copy quantiser, integer bookkeeping and branching kernels.
-#include "rssm_device.cuh"
+#include "slots.cuh"
 
 namespace rssm {
 namespace {
@@ -45,75 +45,15 @@ __global__ void gather_kernel(int B, const int32_t *start, const int32_t *len,
 }
 
 // ------------------------------------------------------------ branching
-// Exclusive prefix sum of one int per thread over the block (blockDim.x a
-// multiple of 32, at most 1024); `total` is the block's sum.
-__device__ __forceinline__ void block_scan(int v, int &excl, int &total) {
-  __shared__ int warp_tot[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  int inc = v;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int t = __shfl_up_sync(kFull, inc, d);
-    if (lane >= d) inc += t;
-  }
-  if (lane == 31) warp_tot[warp] = inc;
-  __syncthreads();
-  if (warp == 0) {
-    int w = lane < nw ? warp_tot[lane] : 0;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int t = __shfl_up_sync(kFull, w, d);
-      if (lane >= d) w += t;
-    }
-    if (lane < nw) warp_tot[lane] = w;   // inclusive over warps
-  }
-  __syncthreads();
-  excl = inc - v + (warp > 0 ? warp_tot[warp - 1] : 0);
-  total = warp_tot[nw - 1];
-  __syncthreads();   // warp_tot is reused by the next call
-}
-
-// A fold of the previous launch wrote row b's new checkpoint to dst[b] and
-// counted itself in flushes[b]: make that slot the row's own.
-__device__ __forceinline__ void adopt_folds(int B, int32_t *slot, const int32_t *dst, int32_t *seen,
-                                            const int32_t *flushes) {
-  for (int b = threadIdx.x; b < B; b += blockDim.x) {
-    const int f = flushes[b];
-    if (f != seen[b]) {
-      slot[b] = dst[b];
-      seen[b] = f;
-    }
-  }
-}
-
 // One CTA.  Slots are 0 .. 2B-1; rows reference at most B of them, so at
 // least B are free and every row that folds in the coming launch gets a
 // distinct free slot: a fold never writes a slot that any row reads.
 __global__ void __launch_bounds__(1024) plan_slots_kernel(const StepArgs a, int32_t *slot, int32_t *dst,
                                                           int32_t *seen, int32_t *freelist) {
-  const int B = a.B, S = 2 * B, nt = blockDim.x;
+  const int B = a.B, nt = blockDim.x;
   adopt_folds(B, slot, dst, seen, a.flushes);
   __syncthreads();
-  for (int s = threadIdx.x; s < S; s += nt) freelist[s] = 1;
-  __syncthreads();
-  for (int b = threadIdx.x; b < B; b += nt) {
-    const int sl = slot[b];
-    if (sl >= 0 && sl < S) freelist[sl] = 0;
-  }
-  __syncthreads();
-  // compact the free slot ids to the front, tile by tile (a tile's flags are
-  // read before any id is written, and ids land at or before their slot)
-  int nfree = 0;
-  for (int s0 = 0; s0 < S; s0 += nt) {
-    const int s = s0 + threadIdx.x;
-    const int flag = s < S ? freelist[s] : 0;
-    __syncthreads();
-    int excl, tot;
-    block_scan(flag, excl, tot);
-    if (flag) freelist[nfree + excl] = s;
-    nfree += tot;
-    __syncthreads();
-  }
+  const int nfree = free_slots(B, slot, freelist);
   int rank = 0;
   for (int b0 = 0; b0 < B; b0 += nt) {
     const int b = b0 + threadIdx.x;

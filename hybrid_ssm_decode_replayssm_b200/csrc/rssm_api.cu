@@ -10,6 +10,7 @@
 
 #include "rssm_internal.h"
 #include "rssm_kda.h"
+#include "rssm_prefill.h"
 
 struct rssm_handle {
   rssm_layer_desc d;
@@ -208,6 +209,73 @@ int check_inputs(const rssm_handle *h, const void *const *in, const void *out) {
 }
 
 int32_t *meta_i32(const rssm_handle *h, size_t off) { return reinterpret_cast<int32_t *>(h->meta + off); }
+
+// Each ring region is [B][outer][cap][entry]: fills outer and the entries'
+// bytes, returns the number of regions.
+int ring_regions(const rssm_handle *h, int (&outer)[5], int (&entry)[5]) {
+  const rssm_layer_desc &d = h->d;
+  const int H = d.nheads;
+  const int esz = d.in_dtype == RSSM_BF16 ? 2 : 4;
+  if (d.kind == RSSM_MAMBA2) {
+    const int o[3] = {H, d.ngroups, H}, e[3] = {d.headdim * esz, d.dstate * esz, 4};
+    for (int r = 0; r < 3; ++r) outer[r] = o[r], entry[r] = e[r];
+    return 3;
+  }
+  if (d.kind == RSSM_KDA) {   // k [H][cap][dk] | v [H][cap][dv] | g [H][cap][dk] fp32 | beta | w [2H][cap][dv/2]
+    const int o[5] = {H, H, H, H, 2 * H};
+    const int e[5] = {d.dstate * esz, d.headdim * esz, d.dstate * 4, 4, d.headdim / 2 * 4};
+    for (int r = 0; r < 5; ++r) outer[r] = o[r], entry[r] = e[r];
+    return 5;
+  }
+  // k [H][cap][dk] | v [2H][cap][dv/2] | g, beta [H][cap] | w [2H][cap][dv/2] fp32
+  const int o[5] = {H, 2 * H, H, H, 2 * H};
+  const int e[5] = {d.dstate * esz, d.headdim / 2 * esz, 4, 4, d.headdim / 2 * 4};
+  for (int r = 0; r < 5; ++r) outer[r] = o[r], entry[r] = e[r];
+  return 5;
+}
+
+rssm::RowsSide rows_side(const rssm_handle *h) {
+  rssm::RowsSide r;
+  std::memset(&r, 0, sizeof r);
+  r.B = h->d.batch;
+  r.hc = h->ckpt;
+  r.codes = h->rc ? h->rc + h->lay.rc_codes_off : nullptr;
+  r.scales = h->rc ? h->rc + h->lay.rc_scales_off : nullptr;
+  for (int i = 0; i < 5; ++i) r.ring[i] = h->buf + h->lay.buf_off[i];
+  r.start = meta_i32(h, h->lay.meta_start_off);
+  r.len = meta_i32(h, h->lay.meta_len_off);
+  r.pending = meta_i32(h, h->lay.meta_pending_off);
+  r.flushes = meta_i32(h, h->lay.meta_flushes_off);
+  if (h->d.branching) {
+    r.slot = meta_i32(h, h->lay.meta_slot_off);
+    r.dst = meta_i32(h, h->lay.meta_dst_off);
+    r.seen = meta_i32(h, h->lay.meta_seen_off);
+    r.freelist = meta_i32(h, h->lay.meta_work_off);
+  }
+  return r;
+}
+
+rssm::RowsArgs rows_args(const rssm_handle *dst, const rssm_handle *src) {
+  rssm::RowsArgs a;
+  std::memset(&a, 0, sizeof a);
+  const rssm_layer_desc &d = dst->d;
+  a.d = rows_side(dst);
+  a.s = rows_side(src);
+  a.same = dst == src;
+  const size_t rows = (size_t)d.nheads * d.headdim, elems = rows * d.dstate;
+  a.hc_words = elems / 4;
+  if (d.read_fmt == RSSM_READ_FP8_E4M3_ROW) {
+    a.code_words = elems / 16;
+    a.scale_bytes = rows * sizeof(float);
+  } else if (d.read_fmt == RSSM_READ_NVFP4) {
+    a.code_words = elems / 32;
+    a.scale_bytes = elems / 16;
+  }
+  a.nreg = ring_regions(dst, a.outer, a.entry_bytes);
+  a.cap = (int)dst->lay.cap;
+  a.status = reinterpret_cast<uint32_t *>(dst->meta + dst->lay.meta_status_off);
+  return a;
+}
 
 // Layers that branch: before each replay launch, give the rows that fold in it
 // a free checkpoint slot (no-op otherwise).
@@ -480,24 +548,7 @@ int rssm_branch(rssm_handle *h, const int32_t *parent_dev, rssm_stream_t stream)
   b.pending = meta_i32(h, h->lay.meta_pending_off);
   b.flushes = meta_i32(h, h->lay.meta_flushes_off);
   b.status = reinterpret_cast<uint32_t *>(h->meta + h->lay.meta_status_off);
-  // each ring region is [B][outer][cap][entry]
-  const int H = d.nheads;
-  const int esz = d.in_dtype == RSSM_BF16 ? 2 : 4;
-  if (d.kind == RSSM_MAMBA2) {
-    const int outer[3] = {H, d.ngroups, H}, entry[3] = {d.headdim * esz, d.dstate * esz, 4};
-    b.nreg = 3;
-    for (int r = 0; r < 3; ++r) b.outer[r] = outer[r], b.entry_bytes[r] = entry[r];
-  } else if (d.kind == RSSM_KDA) {   // k [H][cap][dk] | v [H][cap][dv] | g [H][cap][dk] fp32 | beta | w [2H][cap][dv/2]
-    const int outer[5] = {H, H, H, H, 2 * H};
-    const int entry[5] = {d.dstate * esz, d.headdim * esz, d.dstate * 4, 4, d.headdim / 2 * 4};
-    b.nreg = 5;
-    for (int r = 0; r < 5; ++r) b.outer[r] = outer[r], b.entry_bytes[r] = entry[r];
-  } else {   // k [H][cap][dk] | v [2H][cap][dv/2] | g, beta [H][cap] | w [2H][cap][dv/2] fp32
-    const int outer[5] = {H, 2 * H, H, H, 2 * H};
-    const int entry[5] = {d.dstate * esz, d.headdim / 2 * esz, 4, 4, d.headdim / 2 * 4};
-    b.nreg = 5;
-    for (int r = 0; r < 5; ++r) b.outer[r] = outer[r], b.entry_bytes[r] = entry[r];
-  }
+  b.nreg = ring_regions(h, b.outer, b.entry_bytes);
   b.cap = (int)h->lay.cap;
   for (int r = 0; r < b.nreg; ++r) {
     b.ring[r] = h->buf + h->lay.buf_off[r];
@@ -506,6 +557,122 @@ int rssm_branch(rssm_handle *h, const int32_t *parent_dev, rssm_stream_t stream)
   cudaError_t e = rssm::branch_rows(b, parent_dev, work, (cudaStream_t)stream);
   g_launches.fetch_add(2, std::memory_order_relaxed);
   if (e != cudaSuccess) return cuda_fail(e, "branch launches");
+  return ok();
+}
+
+int rssm_prefill_workspace_size(rssm_handle *h, int n_seq, int n_tokens, size_t *bytes) {
+  const CallRange call_range(__func__);
+  if (!h) return fail(RSSM_ERR_INVALID_ARG, "handle is NULL");
+  if (!bytes) return fail(RSSM_ERR_INVALID_ARG, "bytes is NULL");
+  if (n_seq < 1 || n_seq > h->d.batch)
+    return fail(RSSM_ERR_INVALID_ARG, "n_seq = %d outside [1, batch = %d]", n_seq, h->d.batch);
+  if (n_tokens < 0) return fail(RSSM_ERR_INVALID_ARG, "n_tokens must be >= 0");
+  *bytes = rssm::prefill_work_bytes(h->d, n_seq, n_tokens);
+  return ok();
+}
+
+int rssm_prefill(rssm_handle *h, int n_seq, int n_tokens, const int32_t *offsets_dev, const int32_t *rows_dev,
+                 const int32_t *fresh_dev, const void *const *in, const int64_t *in_strides, void *out_dev,
+                 void *work_dev, size_t work_bytes, rssm_stream_t stream) {
+  const CallRange call_range(__func__);
+  if (!h) return fail(RSSM_ERR_INVALID_ARG, "handle is NULL");
+  const rssm_layer_desc &d = h->d;
+  if (n_seq < 1 || n_seq > d.batch)
+    return fail(RSSM_ERR_INVALID_ARG, "n_seq = %d outside [1, batch = %d]", n_seq, d.batch);
+  if (n_tokens < 0) return fail(RSSM_ERR_INVALID_ARG, "n_tokens must be >= 0");
+  if (!offsets_dev) return fail(RSSM_ERR_INVALID_ARG, "offsets is NULL");
+  if (n_tokens > 0) {
+    int rc = check_inputs(h, in, out_dev);
+    if (rc) return rc;
+  } else if (d.kind == RSSM_MAMBA2 && (!h->A || !h->D)) {
+    return fail(RSSM_ERR_STATE, "Mamba-2 parameters not set (rssm_set_params)");
+  }
+  if (!work_dev || !aligned(work_dev, 256))
+    return fail(RSSM_ERR_INVALID_ARG, "the workspace must be a 256-byte aligned device buffer");
+  const size_t need = rssm::prefill_work_bytes(d, n_seq, n_tokens);
+  if (work_bytes < need) return fail(RSSM_ERR_INVALID_ARG, "workspace has %zu bytes, the call needs %zu", work_bytes, need);
+  rssm::PrefillArgs a;
+  std::memset(&a, 0, sizeof a);
+  const rssm::StepArgs p = step_args(h, rssm::kDecode, 0);
+  a.kind = d.kind;
+  a.B = p.B; a.H = p.H; a.G = p.G; a.hpg = p.hpg; a.R = p.R; a.C = p.C;
+  a.n_seq = n_seq; a.n_tokens = n_tokens;
+  a.out_scale = d.out_scale;
+  a.A = h->A; a.D = h->D;
+  a.hc = h->ckpt;
+  // the elements of one token in each input
+  const int64_t heads = d.nheads, R = d.headdim, C = d.dstate;
+  const int64_t m2[5] = {heads * R, (int64_t)d.ngroups * C, (int64_t)d.ngroups * C, heads, 0};
+  const int64_t dr[5] = {heads * C, heads * C, heads * R, d.kind == RSSM_KDA ? heads * C : heads, heads};
+  const int esz = d.in_dtype == RSSM_BF16 ? 2 : 4;
+  for (int i = 0; i < n_inputs(h); ++i) {
+    const int64_t packed = d.kind == RSSM_MAMBA2 ? m2[i] : dr[i];
+    const bool scalar = d.kind == RSSM_MAMBA2 ? i == 3 : i == 4 || (i == 3 && d.kind == RSSM_GDN);
+    const int size = d.kind != RSSM_MAMBA2 && i >= 3 ? 4 : esz;
+    a.stride[i] = in_strides ? in_strides[i] : packed;
+    a.in[i] = n_tokens > 0 ? in[i] : nullptr;
+    if (a.stride[i] < packed)
+      return fail(RSSM_ERR_INVALID_ARG, "in_strides[%d] = %lld is less than a token's %lld elements", i,
+                  (long long)a.stride[i], (long long)packed);
+    if (!scalar && a.stride[i] * size % 16)
+      return fail(RSSM_ERR_INVALID_ARG, "in_strides[%d]: tokens must be a multiple of 16 bytes apart", i);
+  }
+  a.out = static_cast<float *>(out_dev);
+  a.offsets = offsets_dev; a.rows = rows_dev; a.fresh = fresh_dev;
+  a.len = p.len; a.pending = p.pending; a.flushes = p.flushes; a.status = p.status;
+  if (d.branching) {
+    a.slot = meta_i32(h, h->lay.meta_slot_off);
+    a.dst = meta_i32(h, h->lay.meta_dst_off);
+    a.seen = meta_i32(h, h->lay.meta_seen_off);
+    a.freelist = meta_i32(h, h->lay.meta_work_off);
+  }
+  a.rc_codes = p.rc_codes; a.rc_scales = p.rc_scales;
+  a.wait_limit = h->wait_limit;
+  int launches = 0;
+  const cudaError_t e = rssm::prefill(a, work_dev, d.in_dtype, d.read_fmt, &launches, (cudaStream_t)stream);
+  g_launches.fetch_add(launches, std::memory_order_relaxed);
+  if (e != cudaSuccess) return cuda_fail(e, "prefill launches");
+  return ok();
+}
+
+int rssm_copy_rows(rssm_handle *dst, rssm_handle *src, int n, const int32_t *dst_rows_dev,
+                   const int32_t *src_rows_dev, rssm_stream_t stream) {
+  const CallRange call_range(__func__);
+  if (!dst || !src) return fail(RSSM_ERR_INVALID_ARG, "handle is NULL");
+  const rssm_layer_desc &a = dst->d, &b = src->d;
+  if (a.kind != b.kind || a.nheads != b.nheads || (a.kind == RSSM_MAMBA2 && a.ngroups != b.ngroups) ||
+      a.headdim != b.headdim || a.dstate != b.dstate || a.window != b.window || dst->lay.cap != src->lay.cap ||
+      a.in_dtype != b.in_dtype || a.read_fmt != b.read_fmt)
+    return fail(RSSM_ERR_INVALID_ARG, "the layers' rows differ (kind, shape, window, ring capacity, input type or read format)");
+  if (n < 1 || n > a.batch) return fail(RSSM_ERR_INVALID_ARG, "n = %d outside [1, batch = %d]", n, a.batch);
+  if (!dst_rows_dev || !src_rows_dev) return fail(RSSM_ERR_INVALID_ARG, "dst_rows or src_rows is NULL");
+  rssm::RowsArgs r = rows_args(dst, src);
+  r.n = n;
+  r.dst_rows = dst_rows_dev;
+  r.src_rows = src_rows_dev;
+  int launches = 0;
+  const cudaError_t e = rssm::copy_rows(r, &launches, (cudaStream_t)stream);
+  g_launches.fetch_add(launches, std::memory_order_relaxed);
+  if (e != cudaSuccess) return cuda_fail(e, "row copy launches");
+  return ok();
+}
+
+int rssm_compact_rows(rssm_handle *h, const int32_t *live_dev, int32_t *new_row_dev, int32_t *n_live_dev,
+                      rssm_stream_t stream) {
+  const CallRange call_range(__func__);
+  if (!h) return fail(RSSM_ERR_INVALID_ARG, "handle is NULL");
+  if (!live_dev || !new_row_dev || !n_live_dev)
+    return fail(RSSM_ERR_INVALID_ARG, "live, new_row or n_live is NULL");
+  if (live_dev == new_row_dev || live_dev == n_live_dev)
+    return fail(RSSM_ERR_INVALID_ARG, "live must not be an output");
+  rssm::RowsArgs r = rows_args(h, h);
+  r.live = live_dev;
+  r.new_row = new_row_dev;
+  r.n_live = n_live_dev;
+  int launches = 0;
+  const cudaError_t e = rssm::compact_rows(r, &launches, (cudaStream_t)stream);
+  g_launches.fetch_add(launches, std::memory_order_relaxed);
+  if (e != cudaSuccess) return cuda_fail(e, "row compaction launches");
   return ok();
 }
 

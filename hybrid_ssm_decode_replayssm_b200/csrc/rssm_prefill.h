@@ -1,0 +1,70 @@
+// Launchers of the prefill scans (prefill.cu) and the row moves (rows.cu) for
+// the C-ABI host code.
+#pragma once
+
+#include "rssm_internal.h"
+
+namespace rssm {
+
+// One sequence of a prefill call as its planner decided it: tokens
+// [tok, tok + n) of the packed inputs, the checkpoint slots it reads (src, -1 =
+// zero state) and writes (dst).  dst = -1: refused, or nothing to do.
+struct PrefillSeq {
+  int32_t tok, n, src, dst;
+};
+
+struct PrefillArgs {
+  int kind;
+  int B, H, G, hpg, R, C;
+  int n_seq, n_tokens;
+  float out_scale;
+  const float *A, *D;
+  float *hc;
+  const void *in[5];
+  int64_t stride[5];          // elements between consecutive tokens
+  float *out;
+  const int32_t *offsets, *rows, *fresh;
+  // workspace: the planned sequences, longest first, and a counter per row
+  PrefillSeq *seqs;
+  int32_t *named;
+  // bookkeeping
+  int32_t *len, *pending, *flushes;
+  int32_t *slot, *dst, *seen, *freelist;   // branching layers only (else NULL)
+  uint32_t *status;
+  // read copy (NULL: none)
+  uint8_t *rc_codes;
+  void *rc_scales;
+  long long wait_limit;
+};
+
+// Bytes of the caller's workspace of one call.
+size_t prefill_work_bytes(const rssm_layer_desc &d, int n_seq, int n_tokens);
+// Binds the workspace in `a` and enqueues the call; *launches counts its kernels.
+cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *launches, cudaStream_t s);
+
+// One side of a row move: the buffers of a layer.
+struct RowsSide {
+  int B;
+  float *hc;
+  uint8_t *codes, *scales;
+  uint8_t *ring[5];
+  int32_t *start, *len, *pending, *flushes;
+  int32_t *slot, *dst, *seen, *freelist;   // branching layers only (else NULL)
+};
+struct RowsArgs {
+  RowsSide d, s;              // destination and source layer (equal: one layer)
+  int same;                   // one layer is both
+  size_t hc_words, code_words, scale_bytes;   // per row: 16-byte words, and bytes of the scales
+  int nreg, cap;
+  int outer[5], entry_bytes[5];
+  uint32_t *status;           // of the destination
+  int n;                      // pairs
+  const int32_t *dst_rows, *src_rows;
+  // rssm_compact_rows
+  const int32_t *live;
+  int32_t *new_row, *n_live;
+};
+cudaError_t copy_rows(const RowsArgs &a, int *launches, cudaStream_t s);
+cudaError_t compact_rows(const RowsArgs &a, int *launches, cudaStream_t s);
+
+}  // namespace rssm

@@ -36,6 +36,7 @@ EXPORTED = [
     "rssm_branch", "rssm_restore", "rssm_get_slots",
     "rssm_state_bytes", "rssm_export_state", "rssm_import_state", "rssm_get_lengths",
     "rssm_set_wait_limit", "rssm_arm_timeout_test",
+    "rssm_prefill_workspace_size", "rssm_prefill", "rssm_copy_rows", "rssm_compact_rows",
 ]
 RSSM_STATIC_SCRATCH_MAX_BATCH = 65536
 
@@ -95,6 +96,10 @@ def lib():
         L.rssm_export_state.argtypes = [vp, vp, sz, vp]
         L.rssm_import_state.argtypes = [vp, vp, sz, vp]
         L.rssm_get_status.argtypes = [vp, C.POINTER(C.c_uint32), i32, vp]
+        L.rssm_prefill_workspace_size.argtypes = [vp, i32, i32, C.POINTER(sz)]
+        L.rssm_prefill.argtypes = [vp, i32, i32, vp, vp, vp, C.POINTER(vp), C.POINTER(C.c_int64), vp, vp, sz, vp]
+        L.rssm_copy_rows.argtypes = [vp, vp, i32, vp, vp, vp]
+        L.rssm_compact_rows.argtypes = [vp, vp, vp, vp, vp]
         for name in EXPORTED:
             getattr(L, name).restype = C.c_int
         L.rssm_last_error_string.restype = C.c_char_p
@@ -236,6 +241,85 @@ class ReplayLayer:
     def branch(self, parent, stream=None):
         """Sequence b continues from sequence parent[b] (device int32 [B])."""
         check(lib().rssm_branch(self.handle, parent.data_ptr(), _stream(stream)))
+
+    def _row_list(self, t, n, name):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.shape != (n,) or \
+                not t.is_contiguous() or t.device != self.ckpt.device:
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape [{n}] on {self.ckpt.device}")
+        return t
+
+    def _token_shapes(self, T):
+        d = self.desc
+        H, R, Cc = d.nheads, d.headdim, d.dstate
+        t = torch.bfloat16 if d.in_dtype == RSSM_BF16 else torch.float32
+        if d.kind == RSSM_MAMBA2:
+            return [((T, H, R), t), ((T, d.ngroups, Cc), t), ((T, d.ngroups, Cc), t), ((T, H), t)]
+        gate = (T, H, Cc) if d.kind == RSSM_KDA else (T, H)
+        return [((T, H, Cc), t), ((T, H, Cc), t), ((T, H, R), t), (gate, torch.float32), ((T, H), torch.float32)]
+
+    def prefill(self, inputs, offsets, out, rows=None, fresh=None, stream=None):
+        """Run prompts through the layer: tokens offsets[i] .. offsets[i + 1] - 1 of the packed
+        inputs ([tokens, H, ...], any stride between tokens) continue row rows[i], or start it
+        anew where fresh[i] is nonzero.  ``out`` [tokens, H, headdim] fp32 gets the outputs."""
+        dev = self.ckpt.device
+        if not isinstance(out, torch.Tensor) or out.dim() != 3:
+            raise ValueError("out must be a [tokens, heads, headdim] tensor")
+        T, n = out.shape[0], offsets.numel() - 1
+        self._row_list(offsets, n + 1, "offsets")
+        for t, name in ((rows, "rows"), (fresh, "fresh")):
+            if t is not None:
+                self._row_list(t, n, name)
+        shapes = self._token_shapes(T)
+        if len(inputs) != len(shapes):
+            raise ValueError(f"the layer takes {len(shapes)} inputs, got {len(inputs)}")
+        strides = (C.c_int64 * 5)()
+        for i, (t, (shape, dtype)) in enumerate(zip(inputs, shapes)):
+            if tuple(t.shape) != shape or t.dtype != dtype or t.device != dev:
+                raise ValueError(f"inputs[{i}] must be {dtype} {list(shape)} on {dev}, "
+                                 f"got {t.dtype} {list(t.shape)} on {t.device}")
+            width = t[0].numel() if T else 0
+            if T and not t[0].is_contiguous():
+                raise ValueError(f"inputs[{i}]: the values of one token must be contiguous")
+            strides[i] = t.stride(0) if T > 1 else width
+        if tuple(out.shape) != (T, self.desc.nheads, self.desc.headdim) or out.dtype != torch.float32 or \
+                out.device != dev or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous fp32 [{T}, {self.desc.nheads}, {self.desc.headdim}] "
+                             f"tensor on {dev}")
+        nbytes = C.c_size_t()
+        check(lib().rssm_prefill_workspace_size(self.handle, n, T, C.byref(nbytes)))
+        with torch.cuda.device(dev):
+            s = torch.cuda.current_stream() if stream is None else stream
+            with torch.cuda.stream(s):   # the workspace belongs to the stream that uses it
+                work = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+            check(lib().rssm_prefill(self.handle, n, T, offsets.data_ptr(), _ptr(rows), _ptr(fresh),
+                                     _ptr_array(inputs), strides if T else None, out.data_ptr(),
+                                     work.data_ptr(), nbytes.value, s.cuda_stream))
+        return out
+
+    def copy_rows(self, src, dst_rows, src_rows, stream=None):
+        """Row src_rows[i] of the layer ``src`` (which may be this one) into row dst_rows[i] of this
+        layer; src_rows[i] = -1 empties the row."""
+        n = dst_rows.numel()
+        self._row_list(dst_rows, n, "dst_rows")
+        self._row_list(src_rows, n, "src_rows")
+        if src.ckpt.device != self.ckpt.device:
+            raise ValueError("both layers must be on one device")
+        with torch.cuda.device(self.ckpt.device):
+            check(lib().rssm_copy_rows(self.handle, src.handle, n, dst_rows.data_ptr(), src_rows.data_ptr(),
+                                       _stream(stream)))
+
+    def compact_rows(self, live, stream=None):
+        """Pack the rows with nonzero ``live`` (int32 [B]) in front; returns (new_row [B], n_live [1])."""
+        B = self.desc.batch
+        self._row_list(live, B, "live")
+        with torch.cuda.device(self.ckpt.device):
+            s = torch.cuda.current_stream() if stream is None else stream
+            with torch.cuda.stream(s):
+                told = torch.empty(B + 1, dtype=torch.int32, device=self.ckpt.device)
+            new_row, n_live = told[:B], told[B:]
+            check(lib().rssm_compact_rows(self.handle, live.data_ptr(), new_row.data_ptr(), n_live.data_ptr(),
+                                          s.cuda_stream))
+        return new_row, n_live
 
     def restore(self, keep, stream=None):
         """Sequence b keeps the first keep[b] committed tokens of its window."""

@@ -366,6 +366,75 @@ int rssm_decode_step_static_scratch(rssm_handle *h, const void *const *in,
 int rssm_branch(rssm_handle *h, const int32_t *parent_dev, rssm_stream_t stream);
 
 /*
+ * Prefill (no passage: the pages decode only; serving needs the states that
+ * decoding starts from).  Runs a batch of prompts through the layer's recurrence:
+ * each sequence starts from its row's checkpoint, or from zero, and leaves its
+ * final state in the row's checkpoint, with an output for every token.
+ *
+ * Tokens are packed: sequence i (0 <= i < n_seq) is tokens offsets[i] ..
+ * offsets[i+1] - 1 of the inputs (device int32 [n_seq + 1], non-decreasing,
+ * inside [0, n_tokens]; it may be empty), and it runs in row rows[i] (device
+ * int32 [n_seq], all different; NULL: row i).  Tokens outside every sequence are
+ * neither read nor written.
+ *   fresh_dev: device int32 [n_seq], nonzero = start from the zero state and
+ *   drop whatever the row held (window and drafts included); NULL or 0 =
+ *   continue the row's checkpoint, whose window must be empty (rssm_flush).
+ *   in[]: as rssm_decode_step with a token axis in place of the batch axis
+ *   ([n_tokens, H, P], ...), 16-byte aligned.  in_strides: host array, elements
+ *   from one token to the next per input (slices of a wider projection); at
+ *   least a token's elements, and a multiple of 16 bytes except for the inputs
+ *   with one value per head; NULL = packed.
+ *   out_dev: fp32 [n_tokens, H, P] / [n_tokens, H, dv], packed.
+ *   n_tokens = 0: in and out are not used and may be NULL.
+ * Afterwards the row's window is empty, its read copy is rebuilt, and the call
+ * counts as one fold (flushes); a sequence without tokens that is not fresh
+ * changes nothing.  Reads always come from the fp32 state.  On a branching
+ * layer the new state goes to a free slot, so rows that share the old one keep
+ * it.  A sequence whose row is out of range or named twice, or that continues a
+ * row with a window, sets RSSM_STATUS_STATE and is skipped, its outputs and row
+ * untouched; offsets that decrease or leave [0, n_tokens] skip all of them.
+ * The workspace (rssm_prefill_workspace_size for the same n_seq and n_tokens;
+ * 256-byte aligned) holds the call's plan: it needs no initialisation and may be
+ * reused by later calls on the same stream, not by calls that may run at once.
+ */
+int rssm_prefill_workspace_size(rssm_handle *h, int n_seq, int n_tokens, size_t *bytes);
+int rssm_prefill(rssm_handle *h, int n_seq, int n_tokens, const int32_t *offsets_dev,
+                 const int32_t *rows_dev, const int32_t *fresh_dev, const void *const *in,
+                 const int64_t *in_strides, void *out_dev, void *work_dev, size_t work_bytes,
+                 rssm_stream_t stream);
+
+/*
+ * Copy rows (no passage: serving needs it to admit, fork, move and free
+ * sequences).  Pair i < n copies the state of row src_rows[i] of `src` --
+ * checkpoint, read copy, window and pointers -- into row dst_rows[i] of `dst`
+ * (device int32 [n] each); src_rows[i] = -1 empties the row instead (zero
+ * state, empty window).  The two handles may be one (rows forked or emptied in
+ * place) or two layers on the same GPU that agree in all but batch, auto_flush,
+ * branching and out_scale (a window is folded with the destination's Mamba-2
+ * parameters, so both must have the same).  One row may be copied to many.
+ * On a branching layer a row copied inside the layer shares its source's slot
+ * (as rssm_branch); any other gets a free slot, so rows that share the old one
+ * keep it.  A pair whose rows are out of range, whose source has pending
+ * drafts, whose destination another pair names too, or (one layer) whose
+ * destination is another pair's source, sets RSSM_STATUS_STATE in `dst` and is
+ * skipped; a row copied to itself is left alone.  n at most dst's batch.
+ */
+int rssm_copy_rows(rssm_handle *dst, rssm_handle *src, int n, const int32_t *dst_rows_dev,
+                   const int32_t *src_rows_dev, rssm_stream_t stream);
+
+/*
+ * Pack the live rows of a layer in front (no passage: serving, when sequences
+ * of a batch have ended).  live_dev: device int32 [B], nonzero = live.  With
+ * n_live of them, every live row below n_live stays, and the live rows behind,
+ * in order, take the dead rows below n_live, in order, as rssm_copy_rows would
+ * copy them (drafts included).  new_row_dev [B] gets each row's new place, -1
+ * for dead rows, and n_live_dev [1] their number; rows n_live and up are left
+ * as they were.  live_dev must not overlap the outputs.
+ */
+int rssm_compact_rows(rssm_handle *h, const int32_t *live_dev, int32_t *new_row_dev,
+                      int32_t *n_live_dev, rssm_stream_t stream);
+
+/*
  * Restore to a position [guide "What a Replay-First Design Implies": the
  * decode loop can return a sequence to an earlier position]: sequence b returns to its
  * state after the first keep_dev[b] committed tokens of its current window

@@ -1,0 +1,232 @@
+"""rssm_prefill against the token-by-token fp64 recurrences: ragged lengths, every layer
+kind and input type, strides, read copies, branching, refusals, graphs and streams."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import DEV, to64
+from hybrid_ssm_decode_replayssm_b200 import rssm
+from oracle import codecs
+from prefill_common import KINDS, TOL, Layer, i32, offsets_of, scaled
+
+pytestmark = pytest.mark.gpu
+
+
+def run(L, lens, rows, fresh, seed=1, first=0, behind=0, tol=TOL, toks=None, what=""):
+    """One prefill call checked whole: outputs, states, rows and outputs left alone, pointers."""
+    off = offsets_of(lens, first)
+    T = off[-1] + behind
+    toks = L.tokens(T, seed) if toks is None else toks
+    dev = [t.to(DEV) for t in toks]
+    for a, b in [(0, first), (off[-1], T)]:           # nothing reads the tokens outside
+        for t in dev:
+            t[a:b] = float("nan")
+    out = torch.full((T, L.H, L.R), -77.0, device=DEV)
+    before = L.rows()
+    books = L.layer.get_bookkeeping().cpu()
+    L.layer.prefill(dev, i32(off), out, rows=i32(rows), fresh=i32(fresh))
+    assert L.layer.get_status() == 0
+    got, after = to64(out), L.rows()
+    assert (got[:first] == -77).all() and (got[off[-1]:] == -77).all()
+    worst = 0.0
+    for i, r in enumerate(rows):
+        S0 = np.zeros_like(L.state[r]) if fresh[i] else L.state[r]
+        S, o = L.ref_run(S0, [t[off[i]:off[i + 1]] for t in toks])
+        e = max(scaled(got[off[i]:off[i + 1]], o), scaled(after[r], S))
+        assert e <= tol, f"{what} sequence {i} of {lens[i]} tokens: {e:.3e} > {tol:.1e}"
+        worst = max(worst, e)
+        L.state[r] = S
+    rest = [r for r in range(L.batch) if r not in rows]
+    assert (after[rest] == before[rest]).all()
+    now = L.layer.get_bookkeeping().cpu()
+    for i, r in enumerate(rows):
+        touched = bool(fresh[i] or lens[i])
+        assert now[1, r] == 0 and now[2, r] == 0 and now[3, r] == books[3, r] + touched
+    return worst
+
+
+LENS = {"one": [1], "tiny": [0, 1, 2, 3], "around 16": [15, 16, 17, 0], "around 64": [63, 64, 65],
+        "around 128": [127, 128, 129], "long and short": [1, 517, 7]}
+
+
+@pytest.mark.parametrize("lens", list(LENS), ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_ragged(kind, dtype, lens):
+    n = LENS[lens]
+    L = Layer(kind, batch=len(n) + 2, heads=3, dtype=dtype, out_scale=0.7)
+    rows = list(range(len(n) + 1, 1, -1))
+    run(L, n, rows, [i % 2 for i in range(len(n))], first=2, behind=3)
+    run(L, n[::-1], rows, [0] * len(n), seed=2, what="continued")
+
+
+@pytest.mark.parametrize("heads,groups,dstate", [(1, 1, 64), (6, 2, 64), (6, 3, 128), (16, 1, 128)])
+def test_mamba2_groups(heads, groups, dstate):
+    for dtype in ("bf16", "f32"):
+        L = Layer("mamba2", batch=3, heads=heads, groups=groups, dstate=dstate, dtype=dtype)
+        run(L, [70, 0, 33], [2, 0, 1], [1, 1, 0])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_default_rows_and_long(kind):
+    L = Layer(kind, batch=2, heads=2)
+    toks = L.tokens(1100, 5)
+    out = torch.zeros((1100, L.H, L.R), device=DEV)
+    L.layer.prefill([t.to(DEV) for t in toks], i32([0, 1100]), out)
+    S, o = L.ref_run(L.state[0], toks)
+    assert scaled(to64(out), o) <= TOL and scaled(L.rows()[0], S) <= TOL
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_token_strides(kind, dtype):
+    """Inputs that are slices of one wider projection give the packed inputs' results."""
+    L, M = (Layer(kind, batch=2, heads=4, dtype=dtype) for _ in range(2))
+    toks = [t.to(DEV) for t in L.tokens(90, 3)]
+    wide = []
+    for i, t in enumerate(toks):
+        w = torch.full((90, t[0].numel() + 16 * (i + 1)), float("nan"), dtype=t.dtype, device=DEV)
+        at = 8 * (i + 1) if t.dtype == torch.bfloat16 else 4 * (i + 1)
+        w[:, at:at + t[0].numel()] = t.reshape(90, -1)
+        wide.append(w[:, at:at + t[0].numel()].unflatten(1, t.shape[1:]) if t.dim() == 3 else w[:, at:at + t.shape[1]])
+    outs = [torch.zeros((90, L.H, L.R), device=DEV) for _ in range(2)]
+    L.layer.prefill(toks, i32([0, 50, 90]), outs[0])
+    M.layer.prefill(wide, i32([0, 50, 90]), outs[1])
+    assert torch.equal(outs[0], outs[1]) and torch.equal(L.layer.ckpt, M.layer.ckpt)
+
+
+@pytest.mark.parametrize("fmt", [rssm.RSSM_READ_FP8_E4M3_ROW, rssm.RSSM_READ_NVFP4])
+@pytest.mark.parametrize("kind", KINDS)
+def test_read_copy_of_the_rows_written(kind, fmt):
+    for dstate in (64, 128) if kind == "mamba2" else (128,):
+        L = Layer(kind, batch=4, heads=2, dstate=dstate, read_fmt=fmt)
+        run(L, [40, 0, 90], [3, 0, 1], [0, 1, 1])
+        codes, scales = (t.clone() for t in L.layer.read_copy_views())
+        L.layer.quantize_read_copy()
+        for got, want in zip((codes, scales), L.layer.read_copy_views()):
+            assert torch.equal(got, want)
+    assert int(codes[0].max()) == 0            # the emptied row
+    ck = L.layer.ckpt.cpu().numpy()[1, 0]
+    if fmt == rssm.RSSM_READ_FP8_E4M3_ROW:
+        want, _ = codecs.fp8_row_quantize(ck)
+        assert (codes[1, 0].cpu().numpy() == want).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_extreme_gates_and_zero_keys(kind):
+    """Gates of 0, of almost 0 and of 1, steps of 0, keys of zeros: no NaN, and the formula's values."""
+    for dtype in ("bf16", "f32"):
+        L = Layer(kind, batch=2, heads=2, dtype=dtype)
+        toks = L.tokens(150, 9)
+        gate = toks[3]
+        if kind == "mamba2":
+            gate[10] = 0.0                      # dt = 0: nothing happens
+            gate[20:24] = 300.0                 # dt A down to -4800: the state is forgotten
+            gate[70:135] = 0.001
+            toks[0][20:24] *= 1e-3
+        else:
+            gate[10] = 0.0
+            gate[20:24] = 1e-30
+            gate[70:135] = 1.0
+            gate[60:62] = 1e-4
+            toks[4][30] = 0.0
+            toks[4][31] = 1.0
+        toks[1][40] = 0.0
+        # gates of 1 keep an error for 65 tokens instead of 14: (65 / 14) TOL
+        run(L, [149, 1], [1, 0], [0, 0], tol=5 * TOL, toks=toks)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_fresh_rows_do_not_read_what_was_there(kind):
+    L = Layer(kind, batch=3, heads=2)
+    L.layer.ckpt[1] = float("nan")
+    L.state[1] = 0
+    run(L, [30, 5], [1, 2], [1, 0])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_refused_sequences_are_left_alone(kind):
+    L = Layer(kind, batch=6, heads=2)
+    toks = [t.to(DEV) for t in L.tokens(40, 4)]
+    one = [t[:6].contiguous() for t in toks]
+    y = torch.empty((6, L.H, L.R), device=DEV)
+    L.layer.decode_step(one, y)                          # every row has a window now
+    L.layer.flush(i32([1, 0, 1, 1, 1, 1]))               # row 1 keeps it
+    base = L.layer.ckpt.clone()
+
+    def call(off, rows, fresh=None):
+        out = torch.full((40, L.H, L.R), -77.0, device=DEV)
+        books = L.layer.get_bookkeeping()
+        L.layer.prefill(toks, i32(off), out, rows=i32(rows), fresh=None if fresh is None else i32(fresh))
+        bits = L.layer.get_status(clear=True)
+        return bits, out, [r for r in range(6) if not torch.equal(L.layer.ckpt[r], base[r])], \
+            (L.layer.get_bookkeeping() - books).abs().sum(0).cpu().tolist()
+
+    bits, out, changed, moved = call([0, 8, 20, 40], [1, 7, -1])           # window; out of range twice
+    assert bits == rssm.RSSM_STATUS_STATE and changed == [] and (out == -77).all() and sum(moved) == 0
+    bits, out, changed, moved = call([0, 8, 8, 40], [2, 2, 3])             # row 2 twice, row 3 once
+    assert bits == rssm.RSSM_STATUS_STATE and changed == [3]
+    assert (out[:8] == -77).all() and (out[8:] != -77).all()
+    for off in ([0, 8, 4, 40], [-1, 8, 20, 40], [0, 8, 20, 41]):
+        base.copy_(L.layer.ckpt)
+        bits, out, changed, moved = call(off, [0, 2, 3])
+        assert bits == rssm.RSSM_STATUS_STATE and changed == [] and (out == -77).all() and sum(moved) == 0
+    bits, out, changed, moved = call([0, 8, 20, 40], [1, 2, 3], [1, 0, 0])  # fresh: the window is dropped
+    assert bits == 0 and changed == [1, 2, 3] and moved[1] > 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_branching_rows_that_share_a_state(kind):
+    L = Layer(kind, batch=4, heads=2, branching=True)
+    run(L, [33], [0], [1])
+    L.layer.branch(i32([0, 0, 0, 3]))
+    L.state[1] = L.state[2] = L.state[0]
+    run(L, [20, 70], [1, 3], [0, 0], seed=7)             # row 1 goes on, rows 0 and 2 keep the prefix
+    run(L, [5, 5, 5, 5], [2, 1, 0, 3], [0, 1, 0, 0], seed=8)
+    slots = L.layer.get_slots().cpu().tolist()
+    assert len(set(slots)) == 4
+    toks = [t.to(DEV) for t in L.tokens(4, 11)]
+    y = torch.empty((4, L.H, L.R), device=DEV)
+    L.layer.decode_step(toks, y)
+    for r in range(4):
+        _, o = L.ref_run(L.state[r], [t[r:r + 1].cpu() for t in toks])
+        assert scaled(to64(y[r:r + 1]), o) <= TOL
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_stream_and_captured_graph(kind):
+    """A captured call replayed on new inputs in the same buffers gives the eager results."""
+    L, M = (Layer(kind, batch=3, heads=2) for _ in range(2))
+    toks = [t.to(DEV) for t in L.tokens(100, 3)]
+    off, rows = i32([0, 64, 100]), i32([2, 0])
+    outs = [torch.zeros((100, L.H, L.R), device=DEV) for _ in range(2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    L.layer.prefill(toks, off, outs[0], rows=rows, stream=side)       # an eager call on another stream
+    side.synchronize()
+    M.layer.prefill(toks, off, outs[1], rows=rows)
+    assert torch.equal(*outs) and torch.equal(L.layer.ckpt, M.layer.ckpt)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.layer.prefill(toks, off, outs[0], rows=rows)
+    for seed in (21, 22):
+        for t, new in zip(toks, L.tokens(100, seed)):
+            t.copy_(new)
+        off[1] = 30 + seed
+        graph.replay()
+        M.layer.prefill(toks, off, outs[1], rows=rows)
+        torch.cuda.synchronize()
+        assert torch.equal(*outs) and torch.equal(L.layer.ckpt, M.layer.ckpt)
+    assert L.layer.get_status() == 0
+
+
+def test_the_same_call_twice_gives_the_same_bits():
+    for kind in KINDS:
+        res = []
+        for _ in range(2):
+            L = Layer(kind, batch=5, heads=4)
+            toks = [t.to(DEV) for t in L.tokens(700, 3)]
+            out = torch.zeros((700, L.H, L.R), device=DEV)
+            L.layer.prefill(toks, i32([0, 100, 101, 400, 650, 700]), out)
+            res.append((out, L.layer.ckpt))
+        assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])

@@ -1,0 +1,125 @@
+"""Host-side checks of rssm_prefill, rssm_copy_rows and rssm_compact_rows: every refusal
+returns its code before anything is enqueued (no GPU used)."""
+import ctypes as C
+
+import pytest
+import torch
+
+from hybrid_ssm_decode_replayssm_b200 import rssm
+
+FAKE = 1 << 20      # a device address that the refused calls never read
+
+
+def _handle(kind=rssm.RSSM_GDN, params=True, **kw):
+    base = dict(batch=4, nheads=8, headdim=128, dstate=128, window=16, max_draft=4, in_dtype=rssm.RSSM_BF16)
+    if kind == rssm.RSSM_MAMBA2:
+        base.update(headdim=64, ngroups=2)
+    base.update(kw)
+    h = C.c_void_p()
+    d = rssm.make_desc(kind, **base)
+    rc = FAKE if base.get("read_fmt") else None
+    assert rssm.lib().rssm_create(C.byref(d), FAKE, FAKE, rc, FAKE, C.byref(h)) == rssm.RSSM_OK
+    if params:
+        assert rssm.lib().rssm_set_params(h, FAKE, FAKE) == rssm.RSSM_OK
+    return h
+
+
+def _prefill(h, n_seq=2, T=64, off=FAKE, rows=FAKE, fresh=None, ins=None, strides=None, out=FAKE, work=FAKE,
+             nbytes=1 << 20, n_in=5):
+    arr = None if ins == "null" else (C.c_void_p * 5)(*(ins or [FAKE] * n_in))
+    st = None if strides is None else (C.c_int64 * 5)(*strides)
+    return rssm.lib().rssm_prefill(h, n_seq, T, off, rows, fresh, arr, st, out, work, nbytes, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n_seq=0), dict(n_seq=5), dict(n_seq=-1), dict(T=-1), dict(off=None), dict(ins="null"),
+    dict(ins=[FAKE, None, FAKE, FAKE, FAKE]), dict(ins=[FAKE, FAKE + 8, FAKE, FAKE, FAKE]), dict(out=None),
+    dict(out=FAKE + 4), dict(work=None), dict(work=FAKE + 16), dict(nbytes=0),
+    dict(strides=[1023, 1024, 1024, 8, 8]), dict(strides=[1024, 1025, 1024, 8, 8]),
+    dict(strides=[1024, 1024, 0, 8, 8]), dict(strides=[1024, 1024, 1024, 7, 8]), dict(strides=[-1024, 1024, 1024, 8, 8]),
+])
+def test_prefill_arguments(kw):
+    h = _handle()
+    before = rssm.lib().rssm_launch_count()
+    assert _prefill(h, **kw) == rssm.RSSM_ERR_INVALID_ARG
+    assert rssm.lib().rssm_last_error_string() and rssm.lib().rssm_launch_count() == before
+    rssm.lib().rssm_destroy(h)
+
+
+def test_prefill_needs_a_handle_and_parameters():
+    assert _prefill(None) == rssm.RSSM_ERR_INVALID_ARG
+    h = _handle(rssm.RSSM_MAMBA2, params=False)
+    for T in (0, 64):
+        assert _prefill(h, T=T) == rssm.RSSM_ERR_STATE
+    rssm.lib().rssm_destroy(h)
+
+
+def test_prefill_workspace_size():
+    h = _handle()
+    n = C.c_size_t()
+    size = rssm.lib().rssm_prefill_workspace_size
+    assert size(h, 4, 1000, C.byref(n)) == rssm.RSSM_OK and n.value > 0
+    assert _prefill(h, n_seq=4, T=1000, nbytes=n.value - 1) == rssm.RSSM_ERR_INVALID_ARG
+    for bad in ((None, 1, 1), (h, 0, 1), (h, 5, 1), (h, 1, -1)):
+        assert size(*bad, C.byref(n)) == rssm.RSSM_ERR_INVALID_ARG
+    assert size(h, 1, 1, None) == rssm.RSSM_ERR_INVALID_ARG
+    rssm.lib().rssm_destroy(h)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(nheads=4), dict(window=8), dict(max_draft=2), dict(in_dtype=rssm.RSSM_F32), dict(read_fmt=rssm.RSSM_READ_NVFP4),
+    dict(kind=rssm.RSSM_KDA), dict(kind=rssm.RSSM_MAMBA2)])
+def test_copy_rows_between_layers_that_differ(kw):
+    a, b = _handle(), _handle(**kw)
+    assert rssm.lib().rssm_copy_rows(a, b, 1, FAKE, FAKE, None) == rssm.RSSM_ERR_INVALID_ARG
+    assert rssm.lib().rssm_copy_rows(b, a, 1, FAKE, FAKE, None) == rssm.RSSM_ERR_INVALID_ARG
+    for h in (a, b):
+        rssm.lib().rssm_destroy(h)
+
+
+def test_row_move_arguments():
+    L, h = rssm.lib(), _handle()
+    bad = [(None, h, 1, FAKE, FAKE), (h, None, 1, FAKE, FAKE), (h, h, 0, FAKE, FAKE), (h, h, 5, FAKE, FAKE),
+           (h, h, 1, None, FAKE), (h, h, 1, FAKE, None)]
+    for args in bad:
+        assert L.rssm_copy_rows(*args, None) == rssm.RSSM_ERR_INVALID_ARG
+    for args in [(None, FAKE, FAKE, FAKE), (h, None, FAKE, FAKE), (h, FAKE, None, FAKE), (h, FAKE, FAKE, None),
+                 (h, FAKE, FAKE, FAKE + 256), (h, FAKE, FAKE + 256, FAKE)]:
+        assert L.rssm_compact_rows(*args, None) == rssm.RSSM_ERR_INVALID_ARG
+    L.rssm_destroy(h)
+
+
+class _Bare(rssm.ReplayLayer):
+    """A layer's Python checks without a GPU: host tensors, and no call reaches the library."""
+
+    def __init__(self, kind=rssm.RSSM_GDN):
+        self.desc = rssm.make_desc(kind, 4, 2, 128, 128)
+        self.ckpt = torch.zeros(4, 2, 128, 128)
+        self.handle = None
+
+
+def _ok(T=6):
+    t = torch.bfloat16
+    return [torch.zeros(T, 2, 128, dtype=t), torch.zeros(T, 2, 128, dtype=t), torch.zeros(T, 2, 128, dtype=t),
+            torch.zeros(T, 2), torch.zeros(T, 2)]
+
+
+@pytest.mark.parametrize("change", [
+    lambda i, o, r: (i[:4], o, r), lambda i, o, r: ([i[0].float()] + i[1:], o, r),
+    lambda i, o, r: ([i[0][:5]] + i[1:], o, r), lambda i, o, r: ([i[0].transpose(1, 2).contiguous().transpose(1, 2)] + i[1:], o, r),
+    lambda i, o, r: (i, o.bfloat16(), r), lambda i, o, r: (i, o[:, :1], r), lambda i, o, r: (i, o[:, :, :64], r),
+    lambda i, o, r: (i, o, r.long()), lambda i, o, r: (i, o, r[:1]), lambda i, o, r: (i, o.transpose(1, 2), r)])
+def test_python_prefill_checks(change):
+    off = torch.tensor([0, 2, 6], dtype=torch.int32)
+    ins, out, rows = change(_ok(), torch.zeros(6, 2, 128), torch.tensor([0, 1], dtype=torch.int32))
+    with pytest.raises(ValueError):
+        _Bare().prefill(ins, off, out, rows=rows)
+
+
+def test_python_row_checks():
+    L = _Bare()
+    i = torch.zeros(4, dtype=torch.int32)
+    for call in (lambda: L.copy_rows(L, i, i[:2]), lambda: L.copy_rows(L, i.long(), i), lambda: L.compact_rows(i[:3]),
+                 lambda: L.compact_rows(i.bool()), lambda: L.copy_rows(L, [0], [1])):
+        with pytest.raises((ValueError, AttributeError)):
+            call()
