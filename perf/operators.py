@@ -161,11 +161,9 @@ def _state(case, rows, g, full):
             for v, r in zip(views, rings):
                 v.copy_(r)
             rings = views
-            ptrs = [layer.meta[o:o + 4 * rows].view(torch.int32)
-                    for o in (at.meta_start_off, at.meta_len_off, at.meta_pending_off, at.meta_flushes_off)]
-            for v, m in zip(ptrs, meta):
-                v.copy_(m)
-            meta = ptrs
+            # start, len, pending, flushes follow one another in meta, equally far apart
+            ptrs = layer.meta.view(torch.int32).as_strided((4, rows), ((at.meta_len_off - at.meta_start_off) // 4, 1))
+            meta = ptrs.copy_(meta)
             if case["fp8"]:
                 codes, scales = layer.read_copy_views()
                 codes = codes.view(torch.float8_e4m3fn)
