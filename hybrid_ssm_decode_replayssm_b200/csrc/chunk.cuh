@@ -1,0 +1,105 @@
+// Helpers of the chunked prefill kernels: operand tiles in the 128-byte swizzle
+// for tcgen05, operands in tensor memory, the three-part bf16 split of fp32
+// values, and bounded waits that stop the whole CTA.
+#pragma once
+
+#include "rssm_device.cuh"
+#include "umma.cuh"
+
+namespace rssm {
+namespace chunk {
+
+// A tile of 64 bf16 columns is stored as rows of 128 bytes, the 16-byte chunk c
+// of row r at chunk position c ^ (r % 8); wider tiles are several such blocks
+// of columns.  The same bytes serve as an operand whose K runs along a row (K-major:
+// 8-row groups `1024` bytes apart, K = 16 step 32 bytes inside a block) and as one
+// whose K runs over the rows (MN-major: 64-column blocks `lbo` bytes apart, 8-row
+// groups 1024 bytes apart, K = 16 step 2048 bytes).  Blocks start on 1024 bytes.
+__device__ __forceinline__ uint32_t sw128(int row, int c16) {
+  return (uint32_t)(row * 128 + ((c16 ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t smem_addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;   // version
+  d |= (uint64_t)2 << 61;   // 128-byte swizzle
+  return d;
+}
+// kind::f16, D fp32, A and B bf16; a_mn / b_mn: the operand is MN-major.
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// D[tmem] (+)= A[tmem] * B[smem]: A is K-major in tensor memory, lane = row, two
+// consecutive K elements per 32-bit column (K = 16: 8 columns).
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t id, bool acc) {
+  const uint32_t z = 0u;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(id), "r"((uint32_t)acc), "r"(z)
+      : "memory");
+}
+// Store 16 32-bit columns of this warp's lanes.
+__device__ __forceinline__ void st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 values to three bf16 pairs, x = hi + mid + lo to 2^-24 |x| (element 0
+// in the low half); see umma::split3_bf16.
+__device__ __forceinline__ uint32_t pack_bf16(float x0, float x1) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x0, x1);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+  hi = pack_bf16(x0, x1);
+  x0 -= __uint_as_float(hi << 16);
+  x1 -= __uint_as_float(hi & 0xFFFF0000u);
+  mid = pack_bf16(x0, x1);
+  x0 -= __uint_as_float(mid << 16);
+  x1 -= __uint_as_float(mid & 0xFFFF0000u);
+  lo = pack_bf16(x0, x1);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16 bytes global -> shared, zeros where `take` is false (the source is not read).
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Eight consecutive floats, a whole 32-byte sector, to global memory.
+__device__ __forceinline__ void st_sector(float *p, const float *v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// Every lane of the warp arrives through lane 0, its writes before it.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+// All lanes wait; false (for all) once the CTA gives up.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, long long limit) {
+  return warp_all(mbar_wait_bounded(bar, parity, abort, limit));
+}
+
+}  // namespace chunk
+}  // namespace rssm

@@ -1,0 +1,377 @@
+// Chunked Mamba-2 prefill on the 5th-generation tensor cores (bf16 inputs,
+// headdim 64): one CTA per (sequence, head), chunks of 128 tokens.
+//
+// With a_s = dt_s A, G_t = a_1 + .. + a_t inside the chunk and h the state before
+// it ([P, N]; rows t, s are tokens, every sum over one operand's columns):
+//   y  = e^{G_t} (C h^T) + L x + D x,   L_ts = e^{G_t - G_s} dt_s (C B^T)_ts, s <= t
+//   h' = e^{G_last} h + (e^{G_last - G_s} dt_s x_s)^T B
+// as four products per chunk, each with M = 128:
+//   CB    = C B^T            [t, s]  both operands bf16 inputs: exact products
+//   inter = C h^T            [t, p]  h in three bf16 parts
+//   upd   = B^T (fw x)       [n, p]  fw x in three parts: the state's update, transposed
+//   intra = L x              [t, p]  L in three parts, in tensor memory as the A operand
+// (a three-part split carries fp32 to 2^-24, so outputs and states keep fp32
+// accuracy).  The state lives in registers, one column n per thread; it is never
+// scaled in tensor memory.  G is a double prefix sum kept as two floats, so
+// differences of far decays lose nothing.
+//
+// Every barrier completes once per chunk (the stage barriers once per two), and no
+// barrier can complete again before all its waiters have passed: full -> stage freed
+// by y, CB -> L, inter -> y, upd -> the next fw x, decays -> both users.
+//
+// Roles: warps 0-3 (one token per lane) make L from CB and write y; warps 4-7 (one n
+// per lane) make fw x, update the state and split it; warp 8 issues the products;
+// warp 9 computes the decays; warps 10-13 load the tiles with zeros behind the
+// sequence's end, so that nothing past it is ever read.
+#include "chunk.cuh"
+#include "rssm_prefill.h"
+
+namespace rssm {
+namespace {
+
+using namespace chunk;
+
+constexpr int kT = 128;                // tokens per chunk
+constexpr int kP = 64;
+constexpr int kBlk = 16384;            // 128 rows x 64 bf16
+constexpr int kWarpsM = 14;
+constexpr int kThreadsM = kWarpsM * 32;
+// shared memory
+constexpr int kOffB = 0;               // two stages of B, two 64-column blocks each
+constexpr int kOffC = 4 * kBlk;
+constexpr int kOffX = 6 * kBlk;        // two stages
+constexpr int kOffH = 8 * kBlk;        // three parts of the state, [n][p]
+constexpr int kOffXp = 11 * kBlk;      // three parts of fw x, [s][p]
+constexpr int kOffSc = 14 * kBlk;      // float4 (G hi, G lo, dt, fw) per token
+constexpr int kOffBar = kOffSc + kT * 16;
+enum { kFull0 = 0, kFull1, kCb, kInter, kUpd, kIntra, kL, kHp, kXp, kYfree, kScFull, kScFree, kStage0, kStage1,
+       kDrain, kBars };
+constexpr int kSmemM = kOffBar + kBars * 8 + 32;
+static_assert(kSmemM <= 232448, "shared memory of one CTA");
+// tensor memory columns
+constexpr int kTmCb = 0, kTmInter = 128, kTmIntra = 192, kTmU = 256, kTmL = 320;
+
+template <int N>
+__global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const PrefillSeq q = a.seqs[blockIdx.x / a.H];
+  if (q.dst < 0) return;
+  const int h = (int)(blockIdx.x % a.H);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int chunks = (q.n + kT - 1) / kT;
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kOffBar);
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + kOffBar + kBars * 8);
+  uint32_t *tm_slot = reinterpret_cast<uint32_t *>(smem + kOffBar + kBars * 8 + 8);
+  float *s_last = reinterpret_cast<float *>(smem + kOffBar + kBars * 8 + 16);   // e^{G_last}
+  float4 *sc = reinterpret_cast<float4 *>(smem + kOffSc);
+  const uint32_t base = smem_u32(smem);
+  if (t == 0) {
+    const int count[kBars] = {128, 128, 1, 1, 1, 1, 4, 4, 4, 4, 1, 8, 4, 4, 1};
+    for (int i = 0; i < kBars; ++i) mbar_init(bar + i, count[i]);
+    *abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 8) {
+    umma::alloc(tm_slot, 512);
+    umma::relinquish();
+  }
+  if constexpr (N == 64) {   // the second column block of B and C stays zero
+    for (int i = t; i < kBlk / 16; i += kThreadsM) {
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      reinterpret_cast<uint4 *>(smem + kOffB + kBlk)[i] = z;
+      reinterpret_cast<uint4 *>(smem + kOffB + 3 * kBlk)[i] = z;
+      reinterpret_cast<uint4 *>(smem + kOffC + kBlk)[i] = z;
+    }
+    fence_proxy_async();
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tm = *tm_slot;
+  const long long lim = a.wait_limit;
+  const float *src = a.hc + ((size_t)(q.src < 0 ? 0 : q.src) * a.H + h) * kP * N;
+  float *dst = a.hc + ((size_t)q.dst * a.H + h) * kP * N;
+
+  if (warp < 4) {
+    // ------------------------------------------------ L, and the outputs
+    const uint32_t lanes = tm + ((uint32_t)(warp * 32) << 16);
+    uint32_t z[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) z[j] = 0u;
+    for (int cb = warp + 1; cb < 4; ++cb)   // above the diagonal L stays zero
+      for (int p = 0; p < 3; ++p) st_x16(lanes + kTmL + p * 64 + cb * 16, z);
+    const float Dh = __ldg(a.D + h);
+    for (int i = 0; i < chunks; ++i) {
+      const uint32_t ph = i & 1;
+      if (!warp_wait(bar + kScFull, ph, abort, lim) || !warp_wait(bar + kCb, ph, abort, lim)) break;
+      umma::fence_after_sync();
+      const float4 me = sc[t];
+      for (int cb = 0; cb <= warp; ++cb) {
+        float v[32];
+        umma::ld_32x32b_x32(lanes + kTmCb + cb * 32, v);
+        uint32_t hi[16], mid[16], lo[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          const float4 s0 = sc[cb * 32 + j], s1 = sc[cb * 32 + j + 1];
+          float e0 = ex2((me.x - s0.x) + (me.y - s0.y)) * (s0.z * v[j]);
+          float e1 = ex2((me.x - s1.x) + (me.y - s1.y)) * (s1.z * v[j + 1]);
+          if (cb == warp) {
+            e0 = j <= lane ? e0 : 0.f;
+            e1 = j + 1 <= lane ? e1 : 0.f;
+          }
+          split3(e0, e1, hi[j / 2], mid[j / 2], lo[j / 2]);
+        }
+        st_x16(lanes + kTmL + cb * 16, hi);
+        st_x16(lanes + kTmL + 64 + cb * 16, mid);
+        st_x16(lanes + kTmL + 128 + cb * 16, lo);
+      }
+      wait_st();
+      umma::fence_before_sync();
+      warp_arrive(bar + kL);
+      warp_arrive(bar + kScFree);
+      if (!warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim) || !warp_wait(bar + kInter, ph, abort, lim)) break;
+      umma::fence_after_sync();
+      const float g = ex2(me.x + me.y);
+      const uint8_t *xrow = smem + kOffX + (i & 1) * kBlk;
+      float y[kP];
+#pragma unroll
+      for (int c = 0; c < kP; c += 32) {
+        float v[32];
+        umma::ld_32x32b_x32(lanes + kTmInter + c, v);
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          const uint4 raw = *reinterpret_cast<const uint4 *>(xrow + sw128(t, (c + j) / 8));
+          const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            y[c + j + 2 * k] = fmaf(g, v[j + 2 * k], Dh * __uint_as_float(w[k] << 16));
+            y[c + j + 2 * k + 1] = fmaf(g, v[j + 2 * k + 1], Dh * __uint_as_float(w[k] & 0xFFFF0000u));
+          }
+        }
+      }
+      if (!warp_wait(bar + kIntra, ph, abort, lim)) break;
+      umma::fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < kP; c += 32) {
+        float v[32];
+        umma::ld_32x32b_x32(lanes + kTmIntra + c, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[c + j] += v[j];
+      }
+      umma::fence_before_sync();
+      warp_arrive(bar + kYfree);
+      warp_arrive(bar + kStage0 + (i & 1));
+      if (i * kT + t < q.n) {
+        float *o = a.out + ((size_t)(q.tok + i * kT + t) * a.H + h) * kP;
+#pragma unroll
+        for (int c = 0; c < kP; c += 8) st_sector(o + c, y + c);
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------ the state
+    const int n = t - 128;
+    const uint32_t lanes = tm + ((uint32_t)((warp - 4) * 32) << 16);
+    float S[kP];
+#pragma unroll
+    for (int p = 0; p < kP; ++p) S[p] = q.src < 0 || n >= N ? 0.f : __ldcs(src + (size_t)p * N + n);
+    auto put = [&](int part_off, int row, const float *v8, int c16) {   // 8 values -> three parts
+      uint4 w[3];
+      uint32_t *u = reinterpret_cast<uint32_t *>(w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) split3(v8[2 * k], v8[2 * k + 1], u[k], u[4 + k], u[8 + k]);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4 *>(smem + part_off + p * kBlk + sw128(row, c16)) = w[p];
+    };
+    bool good = true;
+    for (int i = 0; i < chunks; ++i) {
+      const uint32_t ph = i & 1;
+#pragma unroll
+      for (int c = 0; c < kP; c += 8) put(kOffH, n, S + c, c / 8);
+      fence_proxy_async();
+      warp_arrive(bar + kHp);
+      good = warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim) && warp_wait(bar + kScFull, ph, abort, lim);
+      if (!good) break;
+      const float dec = *s_last;
+      const uint8_t *x = smem + kOffX + (i & 1) * kBlk;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int s = k * 16 + n / 8, c16 = n % 8;
+        const float fw = sc[s].w;
+        const uint4 raw = *reinterpret_cast<const uint4 *>(x + sw128(s, c16));
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[2 * j] = fw * __uint_as_float(w[j] << 16);
+          v[2 * j + 1] = fw * __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+        put(kOffXp, s, v, c16);
+      }
+      fence_proxy_async();
+      warp_arrive(bar + kXp);
+      warp_arrive(bar + kScFree);
+      good = warp_wait(bar + kUpd, ph, abort, lim);
+      if (!good) break;
+      umma::fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < kP; c += 32) {
+        float v[32];
+        umma::ld_32x32b_x32(lanes + kTmU + c, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) S[c + j] = fmaf(dec, S[c + j], v[j]);
+      }
+      umma::fence_before_sync();
+    }
+    if (good && n < N)
+#pragma unroll
+      for (int p = 0; p < kP; ++p) dst[(size_t)p * N + n] = S[p];
+  } else if (warp == 8) {
+    // ------------------------------------------------ the products
+    constexpr int KN = N / 16;   // K steps along n
+    for (int i = 0; i < chunks; ++i) {
+      const uint32_t ph = i & 1;
+      const uint32_t Bt = base + kOffB + (i & 1) * 2 * kBlk, Ct = base + kOffC, Xt = base + kOffX + (i & 1) * kBlk;
+      auto kmaj = [](uint32_t tile, int k) { return desc_sw128(tile + (k / 4) * kBlk + (k % 4) * 32, 16); };
+      auto mnmaj = [](uint32_t tile, int k) { return desc_sw128(tile + k * 2048, kBlk); };
+      if (!warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim)) break;
+      umma::fence_after_sync();
+      if (lane == 0) {
+        for (int k = 0; k < KN; ++k)
+          umma::mma_bf16(tm + kTmCb, kmaj(Ct, k), kmaj(Bt, k), idesc(128, 128, false, false), k > 0);
+        umma::commit(bar + kCb);
+      }
+      __syncwarp();
+      if (!warp_wait(bar + kHp, ph, abort, lim)) break;
+      if (i > 0 && !warp_wait(bar + kYfree, ph ^ 1, abort, lim)) break;
+      umma::fence_after_sync();
+      if (lane == 0) {
+        for (int p = 0; p < 3; ++p)
+          for (int k = 0; k < KN; ++k)
+            umma::mma_bf16(tm + kTmInter, kmaj(Ct, k), mnmaj(base + kOffH + p * kBlk, k), idesc(128, kP, false, true),
+                           p + k > 0);
+        umma::commit(bar + kInter);
+      }
+      __syncwarp();
+      if (!warp_wait(bar + kXp, ph, abort, lim)) break;
+      umma::fence_after_sync();
+      if (lane == 0) {
+        for (int p = 0; p < 3; ++p)
+          for (int k = 0; k < kT / 16; ++k)
+            umma::mma_bf16(tm + kTmU, mnmaj(Bt, k), mnmaj(base + kOffXp + p * kBlk, k), idesc(128, kP, true, true),
+                           p + k > 0);
+        umma::commit(bar + kUpd);
+      }
+      __syncwarp();
+      if (!warp_wait(bar + kL, ph, abort, lim)) break;
+      umma::fence_after_sync();
+      if (lane == 0) {
+        for (int p = 0; p < 3; ++p)
+          for (int k = 0; k < kT / 16; ++k)
+            mma_ts(tm + kTmIntra, tm + kTmL + p * 64 + k * 8, mnmaj(Xt, k), idesc(128, kP, false, true), p + k > 0);
+        umma::commit(bar + kIntra);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------ decays
+    const double Ah = (double)__ldg(a.A + h) * 1.4426950408889634;   // in powers of two
+    const __nv_bfloat16 *pdt = static_cast<const __nv_bfloat16 *>(a.in[3]) + h;
+    auto load = [&](int i, float (&v)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int s = i * kT + lane * 4 + k;
+        v[k] = s < q.n ? __bfloat162float(pdt[(int64_t)(q.tok + s) * a.stride[3]]) : 0.f;
+      }
+    };
+    float dt[4];
+    if (chunks > 0) load(0, dt);
+    for (int i = 0; i < chunks; ++i) {
+      float next[4] = {0.f, 0.f, 0.f, 0.f};
+      if (i + 1 < chunks) load(i + 1, next);
+      double G[4], sum = 0.0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sum += (double)dt[k] * Ah;
+        G[k] = sum;
+      }
+      double inc = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+      }
+      const double before = inc - sum, last = __shfl_sync(0xffffffffu, inc, 31);
+      if (i > 0 && !warp_wait(bar + kScFree, (i - 1) & 1, abort, lim)) break;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const double g = G[k] + before;
+        const float hi = (float)g;
+        sc[lane * 4 + k] = make_float4(hi, (float)(g - (double)hi), dt[k], dt[k] * ex2((float)(last - g)));
+        dt[k] = next[k];
+      }
+      if (lane == 0) *s_last = ex2((float)last);
+      warp_arrive(bar + kScFull);
+    }
+  } else {
+    // ------------------------------------------------ tiles
+    const int l = t - 320;   // 0..127
+    const int g = h / a.hpg;
+    const __nv_bfloat16 *px = static_cast<const __nv_bfloat16 *>(a.in[0]) + (size_t)h * kP;
+    const __nv_bfloat16 *pB = static_cast<const __nv_bfloat16 *>(a.in[1]) + (size_t)g * N;
+    const __nv_bfloat16 *pC = static_cast<const __nv_bfloat16 *>(a.in[2]) + (size_t)g * N;
+    auto tile = [&](uint32_t to, const __nv_bfloat16 *p, int64_t stride, int i, int cols) {
+      const int per = cols / 8;
+      for (int j = l; j < kT * per; j += 128) {
+        const int s = j / per, c = j % per;
+        const bool take = i * kT + s < q.n;
+        const int tok = take ? q.tok + i * kT + s : q.tok;
+        cp_async16_zfill(to + (c / 8) * kBlk + sw128(s, c % 8), p + tok * stride + c * 8, take);
+      }
+    };
+    for (int i = 0; i < chunks; ++i) {
+      const int st = i & 1;
+      if (i > 1 && !warp_wait(bar + kStage0 + st, ((i >> 1) - 1) & 1, abort, lim)) break;
+      tile(base + kOffB + st * 2 * kBlk, pB, a.stride[1], i, N);
+      tile(base + kOffX + st * kBlk, px, a.stride[0], i, kP);
+      if (i > 0 && !warp_wait(bar + kInter, (i - 1) & 1, abort, lim)) break;
+      tile(base + kOffC, pC, a.stride[2], i, N);
+      cp_commit();
+      cp_wait<0>();
+      fence_proxy_async();
+      mbar_arrive(bar + kFull0 + st);
+    }
+    cp_async_wait_all();
+  }
+  // ------------------------------------------------ end
+  __syncwarp();
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  if (warp == 8) {
+    if (*abort) {   // products may still be in flight: wait for them before their memory goes
+      if (lane == 0) {
+        umma::commit(bar + kDrain);
+        mbar_wait_bounded(bar + kDrain, 0, nullptr, lim);
+      }
+      __syncwarp();
+    }
+    umma::dealloc(tm, 512);
+  }
+  if (t == 0 && *abort) atomicOr(a.status, (unsigned)RSSM_STATUS_TIMEOUT);
+}
+
+}  // namespace
+
+bool m2_chunk_path(const PrefillArgs &a, int in_dtype) {
+  return a.kind == RSSM_MAMBA2 && in_dtype == RSSM_BF16 && a.R == kP && (a.C == 64 || a.C == 128);
+}
+
+cudaError_t m2_chunk_prefill(const PrefillArgs &a, cudaStream_t s) {
+  auto kernel = a.C == 64 ? m2_chunk_kernel<64> : m2_chunk_kernel<128>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemM);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)((size_t)a.n_seq * a.H), kThreadsM, kSmemM, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace rssm

@@ -289,7 +289,9 @@ cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *
   ++*launches;
   if (e != cudaSuccess) return e;
   const bool bf16 = in_dtype == RSSM_BF16;
-  switch (a.kind) {
+  if (m2_chunk_path(a, in_dtype))
+    e = m2_chunk_prefill(a, s);
+  else switch (a.kind) {
     case RSSM_MAMBA2:
       bf16 ? launch_scan<RSSM_MAMBA2, __nv_bfloat16>(a, s) : launch_scan<RSSM_MAMBA2, float>(a, s);
       break;
@@ -299,7 +301,7 @@ cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *
     default:
       bf16 ? launch_scan<RSSM_KDA, __nv_bfloat16>(a, s) : launch_scan<RSSM_KDA, float>(a, s);
   }
-  e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaGetLastError();
   ++*launches;
   if (e != cudaSuccess || read_fmt == RSSM_READ_FP32) return e;
   const dim3 grid((unsigned)((size_t)a.n_seq * a.H));

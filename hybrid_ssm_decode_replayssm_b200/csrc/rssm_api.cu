@@ -584,6 +584,7 @@ int rssm_prefill(rssm_handle *h, int n_seq, int n_tokens, const int32_t *offsets
   if (n_tokens > 0) {
     int rc = check_inputs(h, in, out_dev);
     if (rc) return rc;
+    if (!aligned(out_dev, 32)) return fail(RSSM_ERR_INVALID_ARG, "out is not 32-byte aligned");
   } else if (d.kind == RSSM_MAMBA2 && (!h->A || !h->D)) {
     return fail(RSSM_ERR_STATE, "Mamba-2 parameters not set (rssm_set_params)");
   }

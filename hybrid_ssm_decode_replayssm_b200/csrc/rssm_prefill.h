@@ -42,6 +42,10 @@ size_t prefill_work_bytes(const rssm_layer_desc &d, int n_seq, int n_tokens);
 // Binds the workspace in `a` and enqueues the call; *launches counts its kernels.
 cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *launches, cudaStream_t s);
 
+// The chunked Mamba-2 scan (m2_prefill.cu): bf16 inputs, headdim 64.
+bool m2_chunk_path(const PrefillArgs &a, int in_dtype);
+cudaError_t m2_chunk_prefill(const PrefillArgs &a, cudaStream_t s);
+
 // One side of a row move: the buffers of a layer.
 struct RowsSide {
   int B;

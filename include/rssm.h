@@ -384,7 +384,7 @@ int rssm_branch(rssm_handle *h, const int32_t *parent_dev, rssm_stream_t stream)
  *   from one token to the next per input (slices of a wider projection); at
  *   least a token's elements, and a multiple of 16 bytes except for the inputs
  *   with one value per head; NULL = packed.
- *   out_dev: fp32 [n_tokens, H, P] / [n_tokens, H, dv], packed.
+ *   out_dev: fp32 [n_tokens, H, P] / [n_tokens, H, dv], packed, 32-byte aligned.
  *   n_tokens = 0: in and out are not used and may be NULL.
  * Afterwards the row's window is empty, its read copy is rebuilt, and the call
  * counts as one fold (flushes); a sequence without tokens that is not fresh

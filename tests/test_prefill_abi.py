@@ -34,7 +34,7 @@ def _prefill(h, n_seq=2, T=64, off=FAKE, rows=FAKE, fresh=None, ins=None, stride
 @pytest.mark.parametrize("kw", [
     dict(n_seq=0), dict(n_seq=5), dict(n_seq=-1), dict(T=-1), dict(off=None), dict(ins="null"),
     dict(ins=[FAKE, None, FAKE, FAKE, FAKE]), dict(ins=[FAKE, FAKE + 8, FAKE, FAKE, FAKE]), dict(out=None),
-    dict(out=FAKE + 4), dict(work=None), dict(work=FAKE + 16), dict(nbytes=0),
+    dict(out=FAKE + 4), dict(out=FAKE + 16), dict(work=None), dict(work=FAKE + 16), dict(nbytes=0),
     dict(strides=[1023, 1024, 1024, 8, 8]), dict(strides=[1024, 1025, 1024, 8, 8]),
     dict(strides=[1024, 1024, 0, 8, 8]), dict(strides=[1024, 1024, 1024, 7, 8]), dict(strides=[-1024, 1024, 1024, 8, 8]),
 ])
