@@ -52,6 +52,12 @@ __device__ __forceinline__ void st_x16(uint32_t taddr, const uint32_t (&r)[16]) 
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// Store 8 32-bit columns of this warp's lanes.
+__device__ __forceinline__ void st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Two fp32 values to three bf16 pairs, x = hi + mid + lo to 2^-24 |x| (element 0
@@ -68,6 +74,16 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_
   x0 -= __uint_as_float(mid << 16);
   x1 -= __uint_as_float(mid & 0xFFFF0000u);
   lo = pack_bf16(x0, x1);
+}
+
+// Sixteen values to three parts of eight 32-bit columns, `step` columns apart.
+__device__ __forceinline__ void split_store(uint32_t taddr, int step, const float *v) {
+  uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) split3(v[2 * j], v[2 * j + 1], hi[j], mid[j], lo[j]);
+  st_x8(taddr, hi);
+  st_x8(taddr + step, mid);
+  st_x8(taddr + 2 * step, lo);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -89,6 +105,14 @@ __device__ __forceinline__ void st_sector(float *p, const float *v) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
                "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
+}
+
+// One lane of a converged warp.  (A product issued under `lane == 0` costs 50 cycles of
+// issue, under this predicate 32 at N = 64, the tensor core's own time.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // Every lane of the warp arrives through lane 0, its writes before it.

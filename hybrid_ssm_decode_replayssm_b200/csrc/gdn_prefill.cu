@@ -1,0 +1,539 @@
+// Chunked gated delta rule prefill on the 5th-generation tensor cores (GDN, bf16
+// inputs, headdim = dstate = 128): one CTA per (sequence, head), chunks of 64 tokens.
+//
+// With G_t the running log decay inside the chunk, S [dv, dk] the state before it
+// (rows t, s of K, Q, V, W are tokens):
+//   A_ts = b_t e^{G_t - G_s} k_t.k_s (s < t)       T = (I + A)^-1
+//   W = T R,  R_t = b_t (v_t - e^{G_t} S k_t)
+//   O_t = scale (e^{G_t} S q_t + sum_{s<=t} e^{G_t - G_s} (q_t.k_s) w_s)
+//   S' = e^{G_last} S + sum_s (e^{G_last - G_s} w_s) k_s^T
+// Everything that depends on the state is computed transposed, one value row per
+// tensor-memory lane (M = 128), with the fp32 operand in three bf16 parts in tensor
+// memory and the other operand in shared memory:
+//   U^T, Z^T = S [K; Q]^T   three products (K, Q exact in bf16)
+//   W^T = R^T T^T           six (both sides split; the parts below 2^-24 left out)
+//   O^T = W^T M^T           six
+//   S' += (fw W)^T K        three
+// so states and outputs keep fp32 accuracy.  [K; Q] K^T gives A and M; T is made from
+// A in fp32 by one warpgroup, a chunk ahead of its use.
+// Far decays are differences of double prefix sums kept as two floats.
+//
+// Bound by the chain S -> U -> R -> W -> S' of one chunk after the other.
+//
+// Roles: warps 0-7 the chain and the outputs (one value row per lane, two halves of the
+// columns), warps 8-11 A, M and T, warp 12 issues the products, warp 13 the
+// decays, warps 14-15 load the tiles with zeros behind the sequence's end.
+#include "chunk.cuh"
+#include "rssm_prefill.h"
+
+namespace rssm {
+namespace {
+
+using namespace chunk;
+
+constexpr int kT = 64;                      // tokens per chunk
+constexpr int kD = 128;
+constexpr int kBlk = 16384;                 // 128 rows x 64 bf16
+constexpr int kPart = 8192;                 // 64 x 64 bf16
+constexpr int kThreadsG = 512;
+constexpr int kALd = 68, kTLd = 36, kXLd = 20;   // floats per row of A^T, of 32-wide and of 16-wide blocks
+// shared memory
+constexpr int kOffKQ = 0;                   // two stages: rows 0-63 K, 64-127 Q, two column blocks
+constexpr int kOffV = 4 * kBlk;             // two stages [t][dv]
+constexpr int kOffT = kOffV + 2 * kBlk;     // two buffers of three parts, [t][s]
+constexpr int kOffM = kOffT + 6 * kPart;
+constexpr int kOffA = kOffM + 6 * kPart;    // A^T in fp32, [s][t]
+constexpr int kOffTa = kOffA + kT * kALd * 4;      // T's first 32 rows and columns, [row][column]
+constexpr int kOffTb = kOffTa + 32 * kTLd * 4;     // its last 32, [column][row]
+constexpr int kOffX = kOffTb + 32 * kTLd * 4;      // blocks on the way
+constexpr int kOffSc = kOffX + 4 * 16 * kXLd * 4;
+struct Scalars {
+  float2 g[kT];        // G as two floats, in powers of two
+  float2 be[kT];       // (b_t, e^{G_t})
+  float fw[kT];        // e^{G_last - G_t}
+  float last, pad[3];  // e^{G_last}
+};
+constexpr int kOffBar = kOffSc + 2 * (int)sizeof(Scalars);
+enum { kFull0 = 0, kFull1, kStage0, kStage1, kScFull0, kScFull1, kScFree0, kScFree1, kA, kTm, kSp, kU, kQ, kRp, kW,
+       kWp, kFwp, kO, kUpd, kDrain, kBars };
+constexpr int kSmemG = kOffBar + kBars * 8 + 32;
+static_assert(kSmemG <= 232448 && 32 * kTLd <= 4 * 16 * kXLd, "shared memory of one CTA");
+// tensor memory columns.  U^T, then W^T, then the masked product; Z^T; the parts of S,
+// then of fw W; the state's update, before it the parts of R, then of W; [K; Q] K^T
+constexpr int kTmU = 0, kTmZ = 64, kTmS = 128, kTmFw = 128, kTmD = 320, kTmR = 320, kTmW = 320, kTmA = 448;
+
+// Pairs of parts whose product matters in fp32.  Sums run from the small parts to the
+// large: the tensor core truncates each addition, and only those of the last, large
+// parts then count (1.1e-6 of the result's norm in the other order, 8192 tokens).
+__device__ constexpr int kPa[6] = {1, 0, 2, 0, 1, 0}, kPb[6] = {1, 2, 0, 1, 0, 0};
+
+// (4 x NC outputs) sum_k L[k][r..r+3] R[k][c..c+NC-1], k < n: the left operand is stored
+// by columns, the right by rows.
+template <int NC>
+__device__ __forceinline__ void block_product(float (&o)[4][NC], const float *L, int ll, const float *Rr, int lr, int n) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) o[i][c] = 0.f;
+#pragma unroll 8
+  for (int k = 0; k < n; ++k) {
+    const float4 x = *reinterpret_cast<const float4 *>(L + k * ll);
+    float y[NC];
+    if constexpr (NC == 2) {
+      const float2 v = *reinterpret_cast<const float2 *>(Rr + k * lr);
+      y[0] = v.x; y[1] = v.y;
+    } else {
+      y[0] = Rr[k * lr];
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      o[0][c] = fmaf(x.x, y[c], o[0][c]);
+      o[1][c] = fmaf(x.y, y[c], o[1][c]);
+      o[2][c] = fmaf(x.z, y[c], o[2][c]);
+      o[3][c] = fmaf(x.w, y[c], o[3][c]);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const PrefillSeq q = a.seqs[blockIdx.x / a.H];
+  if (q.dst < 0) return;
+  const int h = (int)(blockIdx.x % a.H);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int chunks = (q.n + kT - 1) / kT;
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kOffBar);
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + kOffBar + kBars * 8);
+  uint32_t *tm_slot = reinterpret_cast<uint32_t *>(smem + kOffBar + kBars * 8 + 8);
+  Scalars *scs = reinterpret_cast<Scalars *>(smem + kOffSc);
+  const uint32_t base = smem_u32(smem);
+  if (t == 0) {
+    const int count[kBars] = {64, 64, 1, 1, 1, 1, 12, 12, 1, 4, 8, 1, 1, 8, 1, 8, 8, 1, 1, 1};
+    for (int i = 0; i < kBars; ++i) mbar_init(bar + i, count[i]);
+    *abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 12) {
+    umma::alloc(tm_slot, 512);
+    umma::relinquish();
+  }
+  for (int i = t; i < (kOffSc - kOffT) / 16; i += kThreadsG)   // T and M stay zero above the diagonal
+    reinterpret_cast<uint4 *>(smem + kOffT)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tm = *tm_slot;
+  const long long lim = a.wait_limit;
+
+  if (warp < 8) {
+    // -------------------------------------------------------- the chain
+    const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    float S[64];
+    if (q.src < 0) {
+#pragma unroll
+      for (int c = 0; c < 64; ++c) S[c] = 0.f;
+    } else {
+      const float *src = a.hc + (((size_t)q.src * a.H + h) * kD + row) * kD + wg * 64;
+#pragma unroll
+      for (int c = 0; c < 64; c += 4) {
+        const float4 v = ld_stream(src + c);
+        S[c] = v.x; S[c + 1] = v.y; S[c + 2] = v.z; S[c + 3] = v.w;
+      }
+    }
+    bool good = true;
+    for (int i = 0; i < chunks; ++i) {
+      const uint32_t ph = i & 1, sp = (i >> 1) & 1;
+      const Scalars &sc = scs[i & 1];
+#pragma unroll
+      for (int c = 0; c < 64; c += 16) split_store(lanes + kTmS + wg * 32 + c / 2, 64, S + c);
+      wait_st();
+      umma::fence_before_sync();
+      warp_arrive(bar + kSp);
+      good = warp_wait(bar + kScFull0 + (i & 1), sp, abort, lim) &&
+             warp_wait(bar + kFull0 + (i & 1), sp, abort, lim) && warp_wait(bar + kU, ph, abort, lim);
+      if (!good) break;
+      umma::fence_after_sync();
+      const __nv_bfloat16 *pv =
+          reinterpret_cast<const __nv_bfloat16 *>(smem + kOffV + (i & 1) * kBlk) + wg * 32 * kD + row;
+#pragma unroll
+      for (int c = 0; c < 32; c += 16) {   // R for this half's 32 tokens
+        float v[16];
+        umma::ld_32x32b_x16(lanes + kTmU + wg * 32 + c, v);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float4 b = *reinterpret_cast<const float4 *>(&sc.be[wg * 32 + c + j]);
+          v[j] = b.x * fmaf(-b.y, v[j], __bfloat162float(pv[(c + j) * kD]));
+          v[j + 1] = b.z * fmaf(-b.w, v[j + 1], __bfloat162float(pv[(c + j + 1) * kD]));
+        }
+        split_store(lanes + kTmR + wg * 16 + c / 2, 32, v);
+      }
+      wait_st();
+      umma::fence_before_sync();
+      warp_arrive(bar + kRp);
+      good = warp_wait(bar + kW, ph, abort, lim);
+      if (!good) break;
+      umma::fence_after_sync();
+      {
+        float v[32];   // W: first its parts, for the outputs; then those of fw W, for the state
+        umma::ld_32x32b_x32(lanes + kTmU + wg * 32, v);
+#pragma unroll
+        for (int c = 0; c < 32; c += 16) split_store(lanes + kTmW + wg * 16 + c / 2, 32, v + c);
+        wait_st();
+        umma::fence_before_sync();
+        warp_arrive(bar + kWp);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(&sc.fw[wg * 32 + j]);
+          v[j] *= f.x; v[j + 1] *= f.y; v[j + 2] *= f.z; v[j + 3] *= f.w;
+        }
+        good = warp_wait(bar + kQ, ph, abort, lim);   // the parts of S are read
+        if (!good) break;
+        umma::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < 32; c += 16) split_store(lanes + kTmFw + wg * 16 + c / 2, 32, v + c);
+      }
+      wait_st();
+      umma::fence_before_sync();
+      warp_arrive(bar + kFwp);
+      good = warp_wait(bar + kO, ph, abort, lim);
+      if (!good) break;
+      umma::fence_after_sync();
+      {   // the outputs of this half's tokens, a value row per lane
+        const int left = q.n - i * kT - wg * 32;
+        float *o = a.out + ((size_t)(q.tok + i * kT + wg * 32) * a.H + h) * kD + row;
+        const size_t step = (size_t)a.H * kD;
+#pragma unroll
+        for (int c = 0; c < 32; c += 16) {
+          float v[16], z[16];
+          umma::ld_32x32b_x16(lanes + kTmU + wg * 32 + c, v);
+          umma::ld_32x32b_x16(lanes + kTmZ + wg * 32 + c, z);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < left) __stcs(o + (c + j) * step, fmaf(a.out_scale * sc.be[wg * 32 + c + j].y, z[j], v[j]));
+        }
+      }
+      const float dec = sc.last;
+      warp_arrive(bar + kScFree0 + (i & 1));
+      good = warp_wait(bar + kUpd, ph, abort, lim);
+      if (!good) break;
+      umma::fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < 64; c += 16) {
+        float v[16];
+        umma::ld_32x32b_x16(lanes + kTmD + wg * 64 + c, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) S[c + j] = fmaf(dec, S[c + j], v[j]);
+      }
+      umma::fence_before_sync();
+    }
+    if (good) {
+      float *dst = a.hc + (((size_t)q.dst * a.H + h) * kD + row) * kD + wg * 64;
+#pragma unroll
+      for (int c = 0; c < 64; c += 8) st_sector(dst + c, S + c);
+    }
+  } else if (warp < 12) {
+    // -------------------------------------------------------- A, M and T
+    const int w = warp - 8, r = w * 32 + lane;
+    const uint32_t lanes = tm + ((uint32_t)(w * 32) << 16);
+    float *sA = reinterpret_cast<float *>(smem + kOffA), *sTa = reinterpret_cast<float *>(smem + kOffTa);
+    float *sTb = reinterpret_cast<float *>(smem + kOffTb), *sX = reinterpret_cast<float *>(smem + kOffX);
+    for (int i = 0; i < chunks; ++i) {
+      const int buf = i & 1;
+      const Scalars &sc = scs[buf];
+      const bool ok = warp_wait(bar + kScFull0 + buf, (i >> 1) & 1, abort, lim) &&
+                      warp_wait(bar + kA, i & 1, abort, lim) &&
+                      (i < 2 || warp_wait(bar + kStage0 + buf, ((i >> 1) - 1) & 1, abort, lim));   // T and M are read
+      if (named_sync_or(1, 128, !ok)) break;   // the four warps agree; the chunk before's blocks are read
+      umma::fence_after_sync();
+      const int tt = r & 63;
+      const float2 me = sc.g[tt];
+      const float mul = w < 2 ? sc.be[tt].x : a.out_scale;
+      const int top = w < 2 ? tt - 1 : tt;         // last column of this row
+#pragma unroll
+      for (int cb = 0; cb < 4; ++cb) {
+        if (cb >= 2 && (w & 1) == 0) continue;     // above the diagonal
+        float v[16];
+        umma::ld_32x32b_x16(lanes + kTmA + cb * 16, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float2 o = sc.g[cb * 16 + j];
+          v[j] = cb * 16 + j <= top ? mul * (ex2((me.x - o.x) + (me.y - o.y)) * v[j]) : 0.f;
+        }
+        if (w < 2) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sA[(cb * 16 + j) * kALd + tt] = v[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; j += 8) {
+            uint4 o[3];
+            uint32_t *u = reinterpret_cast<uint32_t *>(o);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) split3(v[j + 2 * k], v[j + 2 * k + 1], u[k], u[4 + k], u[8 + k]);
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+              *reinterpret_cast<uint4 *>(smem + kOffM + (buf * 3 + p) * kPart + sw128(tt, cb * 2 + j / 8)) = o[p];
+          }
+        }
+      }
+      umma::fence_before_sync();
+      named_sync(1, 128);
+      warp_arrive(bar + kScFree0 + buf);
+      // T by blocks.  Sixteen-wide diagonal blocks by substitution, one per warp, a column per
+      // lane; then T_10 = -T_11 (A_10 T_00) for pairs of blocks, and again for pairs of those.
+      {
+        const int c = lane & 15;
+        float acc[16], val[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          val[k] = k == c ? 1.f : -acc[k];
+#pragma unroll
+          for (int j = (k + 1) / 4 * 4; j < 16; j += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(sA + (w * 16 + k) * kALd + w * 16 + j);
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (j + e > k) acc[j + e] = fmaf(xs[e], val[k], acc[j + e]);
+          }
+        }
+        if (lane < 16) {
+          const int o = (w & 1) * 16;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            if (w < 2) sTa[(o + k) * kTLd + o + c] = val[k];
+            if (w == 1) sX[c * kXLd + k] = val[k];                    // T_11 by columns
+            if (w == 2) sX[(16 + k) * kXLd + c] = val[k];             // T_22 by rows
+          }
+          if (w >= 2) {
+#pragma unroll
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<float4 *>(sTb + (o + c) * kTLd + o + k) = make_float4(val[k], val[k + 1], val[k + 2], val[k + 3]);
+          }
+        }
+      }
+      named_sync(1, 128);
+      {
+        const int pr = w >> 1, id = r & 63, c = id & 15, r4 = (id >> 4) * 4;
+        float x[4][1];
+        float *sXp = sX + (32 + pr * 16) * kXLd;
+        block_product<1>(x, sA + (pr * 32) * kALd + pr * 32 + 16 + r4, kALd, pr ? sX + 16 * kXLd + c : sTa + c,
+                         pr ? kXLd : kTLd, 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sXp[(r4 + e) * kXLd + c] = x[e][0];
+        named_sync(2 + pr, 64);
+        block_product<1>(x, pr ? sTb + 16 * kTLd + 16 + r4 : sX + r4, pr ? kTLd : kXLd, sXp + c, kXLd, 16);
+        if (pr) {
+          *reinterpret_cast<float4 *>(sTb + c * kTLd + 16 + r4) = make_float4(-x[0][0], -x[1][0], -x[2][0], -x[3][0]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sTa[(16 + r4 + e) * kTLd + c] = -x[e][0];
+        }
+      }
+      named_sync(1, 128);
+      {
+        const int c = (r & 15) * 2, r4 = (r >> 4) * 4;
+        auto put = [&](int row, int col, float v0, float v1) {
+          uint32_t hi, mid, lo;
+          split3(v0, v1, hi, mid, lo);
+          uint8_t *at = smem + kOffT + buf * 3 * kPart + sw128(row, col >> 3) + (col & 7) * 2;
+          *reinterpret_cast<uint32_t *>(at) = hi;
+          *reinterpret_cast<uint32_t *>(at + kPart) = mid;
+          *reinterpret_cast<uint32_t *>(at + 2 * kPart) = lo;
+        };
+        float x[4][2];
+        block_product<2>(x, sA + 32 + r4, kALd, sTa + c, kTLd, 32);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<float2 *>(sX + (r4 + e) * kTLd + c) = make_float2(x[e][0], x[e][1]);
+        const float4 b0 = *reinterpret_cast<const float4 *>(sTb + c * kTLd + r4);
+        const float4 b1 = *reinterpret_cast<const float4 *>(sTb + (c + 1) * kTLd + r4);
+        const float y0[4] = {b0.x, b0.y, b0.z, b0.w}, y1[4] = {b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = *reinterpret_cast<const float2 *>(sTa + (r4 + e) * kTLd + c);
+          put(r4 + e, c, v.x, v.y);
+          put(32 + r4 + e, 32 + c, y0[e], y1[e]);
+        }
+        named_sync(1, 128);
+        block_product<2>(x, sTb + r4, kTLd, sX + c, kTLd, 32);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) put(32 + r4 + e, c, -x[e][0], -x[e][1]);
+      }
+      fence_proxy_async();
+      warp_arrive(bar + kTm);
+    }
+  } else if (warp == 12) {
+    // -------------------------------------------------------- the products
+    auto kmaj = [](uint32_t tile, int k) { return desc_sw128(tile + (k / 4) * kBlk + (k % 4) * 32, 16); };
+    auto mnmaj = [](uint32_t tile, int k) { return desc_sw128(tile + k * 2048, kBlk); };
+    auto gram = [&](int i) {   // [K; Q] K^T
+      const uint32_t kq = base + kOffKQ + (i & 1) * 2 * kBlk;
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          umma::mma_bf16(tm + kTmA, kmaj(kq, k), kmaj(kq, k), idesc(128, kT, false, false), k > 0);
+        umma::commit(bar + kA);
+      }
+      __syncwarp();
+    };
+    auto state_product = [&](uint32_t d, uint32_t tile, uint64_t *done) {   // S (rows of tile)^T
+      if (elect_one()) {
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ts(tm + d, tm + kTmS + p * 64 + k * 8, kmaj(tile, k), idesc(128, kT, false, false), p < 2 || k > 0);
+        umma::commit(done);
+      }
+      __syncwarp();
+    };
+    auto pair_product = [&](uint32_t parts, uint32_t tile, uint64_t *done) {   // into U's place
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < 6; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tm + kTmU, tm + parts + kPa[c] * 32 + k * 8, desc_sw128(tile + kPb[c] * kPart + k * 32, 16),
+                   idesc(128, kT, false, false), c + k > 0);
+        umma::commit(done);
+      }
+      __syncwarp();
+    };
+    bool good = chunks == 0 || warp_wait(bar + kFull0, 0, abort, lim);
+    umma::fence_after_sync();
+    if (good && chunks > 0) gram(0);
+    for (int i = 0; good && i < chunks; ++i) {
+      const uint32_t ph = i & 1;
+      const uint32_t kq = base + kOffKQ + (i & 1) * 2 * kBlk;
+      if (!warp_wait(bar + kSp, ph, abort, lim)) break;
+      umma::fence_after_sync();
+      state_product(kTmU, kq, bar + kU);
+      if (!warp_wait(bar + kTm, ph, abort, lim)) break;
+      if (i + 1 < chunks) {   // while the chain makes R
+        if (!warp_wait(bar + kFull0 + ((i + 1) & 1), ((i + 1) >> 1) & 1, abort, lim)) break;
+        umma::fence_after_sync();
+        gram(i + 1);
+      }
+      if (!warp_wait(bar + kRp, ph, abort, lim)) break;
+      umma::fence_after_sync();
+      pair_product(kTmR, base + kOffT + (i & 1) * 3 * kPart, bar + kW);
+      state_product(kTmZ, kq + kPart, bar + kQ);   // while the chain splits W
+      if (!warp_wait(bar + kWp, ph, abort, lim)) break;
+      umma::fence_after_sync();
+      pair_product(kTmW, base + kOffM + (i & 1) * 3 * kPart, bar + kO);
+      if (!warp_wait(bar + kFwp, ph, abort, lim)) break;
+      umma::fence_after_sync();
+      if (elect_one()) {
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tm + kTmD, tm + kTmFw + p * 32 + k * 8, mnmaj(kq, k), idesc(128, kD, false, true), p < 2 || k > 0);
+        umma::commit(bar + kUpd);
+        umma::commit(bar + kStage0 + (i & 1));
+      }
+      __syncwarp();
+    }
+  } else if (warp == 13) {
+    // -------------------------------------------------------- decays
+    const float *pa = static_cast<const float *>(a.in[3]) + h, *pb = static_cast<const float *>(a.in[4]) + h;
+    auto load = [&](int i, float (&al)[2], float (&be)[2]) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int s = i * kT + lane * 2 + k;
+        const bool take = i < chunks && s < q.n;
+        al[k] = take ? pa[(int64_t)(q.tok + s) * a.stride[3]] : 1.f;
+        be[k] = take ? pb[(int64_t)(q.tok + s) * a.stride[4]] : 0.f;
+      }
+    };
+    float al[2], be[2];
+    load(0, al, be);
+    for (int i = 0; i < chunks; ++i) {
+      float aln[2], ben[2];
+      load(i + 1, aln, ben);
+      double g[2];
+      // a gate of 0 forgets all: any power of two this far down does
+      g[0] = fmax(log2((double)al[0]), -16384.0);
+      g[1] = g[0] + fmax(log2((double)al[1]), -16384.0);
+      double inc = g[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+      }
+      const double before = inc - g[1], last = __shfl_sync(0xffffffffu, inc, 31);
+      if (i > 1 && !warp_wait(bar + kScFree0 + (i & 1), ((i >> 1) - 1) & 1, abort, lim)) break;
+      Scalars &sc = scs[i & 1];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const double G = g[k] + before;
+        const float hi = (float)G;
+        sc.g[lane * 2 + k] = make_float2(hi, (float)(G - (double)hi));
+        sc.be[lane * 2 + k] = make_float2(be[k], ex2((float)G));
+        sc.fw[lane * 2 + k] = ex2((float)(last - G));
+        al[k] = aln[k];
+        be[k] = ben[k];
+      }
+      if (lane == 0) sc.last = ex2((float)last);
+      warp_arrive(bar + kScFull0 + (i & 1));
+    }
+  } else {
+    // -------------------------------------------------------- tiles
+    const int l = t - 448;   // 0..63
+    const __nv_bfloat16 *in[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) in[k] = static_cast<const __nv_bfloat16 *>(a.in[k]) + (size_t)h * kD;
+    for (int i = 0; i < chunks; ++i) {
+      const int st = i & 1;
+      if (i > 1 && !warp_wait(bar + kStage0 + st, ((i >> 1) - 1) & 1, abort, lim)) break;
+      const uint32_t kq = base + kOffKQ + st * 2 * kBlk, v = base + kOffV + st * kBlk;
+      for (int j = l; j < kT * 16; j += 64) {
+        const int s = j >> 4, c = j & 15;
+        const bool take = i * kT + s < q.n;
+        const int64_t tok = take ? q.tok + i * kT + s : q.tok;
+        const uint32_t to = kq + (c >> 3) * kBlk;
+        cp_async16_zfill(to + sw128(s, c & 7), in[1] + tok * a.stride[1] + c * 8, take);
+        cp_async16_zfill(to + sw128(64 + s, c & 7), in[0] + tok * a.stride[0] + c * 8, take);
+        cp_async16_zfill(v + s * 256 + c * 16, in[2] + tok * a.stride[2] + c * 8, take);
+      }
+      cp_commit();
+      cp_wait<0>();
+      fence_proxy_async();
+      mbar_arrive(bar + kFull0 + st);
+    }
+    cp_async_wait_all();
+  }
+  // -------------------------------------------------------- end
+  __syncwarp();
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  if (warp == 12) {
+    if (*abort) {   // products may still be in flight: wait for them before their memory goes
+      if (lane == 0) {
+        umma::commit(bar + kDrain);
+        mbar_wait_bounded(bar + kDrain, 0, nullptr, lim);
+      }
+      __syncwarp();
+    }
+    umma::dealloc(tm, 512);
+  }
+  if (t == 0 && *abort) atomicOr(a.status, (unsigned)RSSM_STATUS_TIMEOUT);
+}
+
+}  // namespace
+
+bool gdn_chunk_path(const PrefillArgs &a, int in_dtype) {
+  return a.kind == RSSM_GDN && in_dtype == RSSM_BF16 && a.R == kD && a.C == kD;
+}
+
+cudaError_t gdn_chunk_prefill(const PrefillArgs &a, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemG);
+  if (e != cudaSuccess) return e;
+  gdn_chunk_kernel<<<(unsigned)((size_t)a.n_seq * a.H), kThreadsG, kSmemG, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace rssm

@@ -291,6 +291,8 @@ cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *
   const bool bf16 = in_dtype == RSSM_BF16;
   if (m2_chunk_path(a, in_dtype))
     e = m2_chunk_prefill(a, s);
+  else if (gdn_chunk_path(a, in_dtype))
+    e = gdn_chunk_prefill(a, s);
   else switch (a.kind) {
     case RSSM_MAMBA2:
       bf16 ? launch_scan<RSSM_MAMBA2, __nv_bfloat16>(a, s) : launch_scan<RSSM_MAMBA2, float>(a, s);

@@ -46,6 +46,10 @@ cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *
 bool m2_chunk_path(const PrefillArgs &a, int in_dtype);
 cudaError_t m2_chunk_prefill(const PrefillArgs &a, cudaStream_t s);
 
+// The chunked gated delta rule (gdn_prefill.cu): GDN, bf16 inputs.
+bool gdn_chunk_path(const PrefillArgs &a, int in_dtype);
+cudaError_t gdn_chunk_prefill(const PrefillArgs &a, cudaStream_t s);
+
 // One side of a row move: the buffers of a layer.
 struct RowsSide {
   int B;
