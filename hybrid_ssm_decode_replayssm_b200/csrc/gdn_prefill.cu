@@ -49,12 +49,14 @@ constexpr int kOffX = kOffTb + 32 * kTLd * 4;      // blocks on the way
 constexpr int kOffSc = kOffX + 4 * 16 * kXLd * 4;
 struct Scalars {
   float2 g[kT];        // G as two floats, in powers of two
-  float2 be[kT];       // (b_t, e^{G_t})
+  float be[kT];        // b_t
+  float bg[kT];        // b_t e^{G_t}
+  float zg[kT];        // scale e^{G_t}
   float fw[kT];        // e^{G_last - G_t}
   float last, pad[3];  // e^{G_last}
 };
 constexpr int kOffBar = kOffSc + 2 * (int)sizeof(Scalars);
-enum { kFull0 = 0, kFull1, kStage0, kStage1, kScFull0, kScFull1, kScFree0, kScFree1, kA, kTm, kSp, kU, kQ, kRp, kW,
+enum { kFull0 = 0, kFull1, kStage0, kStage1, kScFull0, kScFull1, kScFree0, kScFree1, kA, kTm, kSp0, kSp1, kU, kQ, kRp, kW,
        kWp, kFwp, kO, kUpd, kDrain, kBars };
 constexpr int kSmemG = kOffBar + kBars * 8 + 32;
 static_assert(kSmemG <= 232448 && 32 * kTLd <= 4 * 16 * kXLd, "shared memory of one CTA");
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
   Scalars *scs = reinterpret_cast<Scalars *>(smem + kOffSc);
   const uint32_t base = smem_u32(smem);
   if (t == 0) {
-    const int count[kBars] = {64, 64, 1, 1, 1, 1, 12, 12, 1, 4, 8, 1, 1, 8, 1, 8, 8, 1, 1, 1};
+    const int count[kBars] = {64, 64, 1, 1, 1, 1, 12, 12, 1, 4, 8, 8, 1, 1, 8, 1, 8, 8, 1, 1, 1};
     for (int i = 0; i < kBars; ++i) mbar_init(bar + i, count[i]);
     *abort = 0;
     mbar_fence_init();
@@ -142,32 +144,54 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
         S[c] = v.x; S[c + 1] = v.y; S[c + 2] = v.z; S[c + 3] = v.w;
       }
     }
+    auto put_state = [&](int c) { split_store(lanes + kTmS + wg * 32 + c / 2, 64, S + c); };
+    auto state_ready = [&](int half) {
+      wait_st();
+      umma::fence_before_sync();
+      warp_arrive(bar + kSp0 + half);
+    };
     bool good = true;
+    if (chunks > 0) {
+#pragma unroll
+      for (int c = 0; c < 64; c += 16) {
+        put_state(c);
+        if (c & 16) state_ready(c >> 5);
+      }
+    }
     for (int i = 0; i < chunks; ++i) {
       const uint32_t ph = i & 1, sp = (i >> 1) & 1;
       const Scalars &sc = scs[i & 1];
+      good = warp_wait(bar + kScFull0 + (i & 1), sp, abort, lim) && warp_wait(bar + kFull0 + (i & 1), sp, abort, lim);
+      if (!good) break;
+      float v[32];   // b v of this half's 32 tokens
+      {
+        const __nv_bfloat16 *pv =
+            reinterpret_cast<const __nv_bfloat16 *>(smem + kOffV + (i & 1) * kBlk) + wg * 32 * kD + row;
 #pragma unroll
-      for (int c = 0; c < 64; c += 16) split_store(lanes + kTmS + wg * 32 + c / 2, 64, S + c);
-      wait_st();
-      umma::fence_before_sync();
-      warp_arrive(bar + kSp);
-      good = warp_wait(bar + kScFull0 + (i & 1), sp, abort, lim) &&
-             warp_wait(bar + kFull0 + (i & 1), sp, abort, lim) && warp_wait(bar + kU, ph, abort, lim);
+        for (int j = 0; j < 32; j += 4) {
+          const float4 b = *reinterpret_cast<const float4 *>(&sc.be[wg * 32 + j]);
+          v[j] = b.x * __bfloat162float(pv[j * kD]);
+          v[j + 1] = b.y * __bfloat162float(pv[(j + 1) * kD]);
+          v[j + 2] = b.z * __bfloat162float(pv[(j + 2) * kD]);
+          v[j + 3] = b.w * __bfloat162float(pv[(j + 3) * kD]);
+        }
+      }
+      good = warp_wait(bar + kU, ph, abort, lim);
       if (!good) break;
       umma::fence_after_sync();
-      const __nv_bfloat16 *pv =
-          reinterpret_cast<const __nv_bfloat16 *>(smem + kOffV + (i & 1) * kBlk) + wg * 32 * kD + row;
 #pragma unroll
-      for (int c = 0; c < 32; c += 16) {   // R for this half's 32 tokens
-        float v[16];
-        umma::ld_32x32b_x16(lanes + kTmU + wg * 32 + c, v);
+      for (int c = 0; c < 32; c += 16) {   // R
+        float u[16];
+        umma::ld_32x32b_x16(lanes + kTmU + wg * 32 + c, u);
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float4 b = *reinterpret_cast<const float4 *>(&sc.be[wg * 32 + c + j]);
-          v[j] = b.x * fmaf(-b.y, v[j], __bfloat162float(pv[(c + j) * kD]));
-          v[j + 1] = b.z * fmaf(-b.w, v[j + 1], __bfloat162float(pv[(c + j + 1) * kD]));
+        for (int j = 0; j < 16; j += 4) {
+          const float4 b = *reinterpret_cast<const float4 *>(&sc.bg[wg * 32 + c + j]);
+          v[c + j] = fmaf(-b.x, u[j], v[c + j]);
+          v[c + j + 1] = fmaf(-b.y, u[j + 1], v[c + j + 1]);
+          v[c + j + 2] = fmaf(-b.z, u[j + 2], v[c + j + 2]);
+          v[c + j + 3] = fmaf(-b.w, u[j + 3], v[c + j + 3]);
         }
-        split_store(lanes + kTmR + wg * 16 + c / 2, 32, v);
+        split_store(lanes + kTmR + wg * 16 + c / 2, 32, v + c);
       }
       wait_st();
       umma::fence_before_sync();
@@ -175,8 +199,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       good = warp_wait(bar + kW, ph, abort, lim);
       if (!good) break;
       umma::fence_after_sync();
-      {
-        float v[32];   // W: first its parts, for the outputs; then those of fw W, for the state
+      {   // W: first its parts, for the outputs; then those of fw W, for the state
         umma::ld_32x32b_x32(lanes + kTmU + wg * 32, v);
 #pragma unroll
         for (int c = 0; c < 32; c += 16) split_store(lanes + kTmW + wg * 16 + c / 2, 32, v + c);
@@ -206,12 +229,20 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
         const size_t step = (size_t)a.H * kD;
 #pragma unroll
         for (int c = 0; c < 32; c += 16) {
-          float v[16], z[16];
-          umma::ld_32x32b_x16(lanes + kTmU + wg * 32 + c, v);
+          float u[16], z[16];
+          umma::ld_32x32b_x16(lanes + kTmU + wg * 32 + c, u);
           umma::ld_32x32b_x16(lanes + kTmZ + wg * 32 + c, z);
 #pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 g = *reinterpret_cast<const float4 *>(&sc.zg[wg * 32 + c + j]);
+            u[j] = fmaf(g.x, z[j], u[j]);
+            u[j + 1] = fmaf(g.y, z[j + 1], u[j + 1]);
+            u[j + 2] = fmaf(g.z, z[j + 2], u[j + 2]);
+            u[j + 3] = fmaf(g.w, z[j + 3], u[j + 3]);
+          }
+#pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (c + j < left) __stcs(o + (c + j) * step, fmaf(a.out_scale * sc.be[wg * 32 + c + j].y, z[j], v[j]));
+            if (c + j < left) __stcs(o + (c + j) * step, u[j]);
         }
       }
       const float dec = sc.last;
@@ -219,14 +250,18 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       good = warp_wait(bar + kUpd, ph, abort, lim);
       if (!good) break;
       umma::fence_after_sync();
+      const bool more = i + 1 < chunks;
 #pragma unroll
       for (int c = 0; c < 64; c += 16) {
-        float v[16];
-        umma::ld_32x32b_x16(lanes + kTmD + wg * 64 + c, v);
+        float d[16];
+        umma::ld_32x32b_x16(lanes + kTmD + wg * 64 + c, d);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) S[c + j] = fmaf(dec, S[c + j], v[j]);
+        for (int j = 0; j < 16; ++j) S[c + j] = fmaf(dec, S[c + j], d[j]);
+        if (more) {
+          put_state(c);
+          if (c & 16) state_ready(c >> 5);
+        }
       }
-      umma::fence_before_sync();
     }
     if (good) {
       float *dst = a.hc + (((size_t)q.dst * a.H + h) * kD + row) * kD + wg * 64;
@@ -249,7 +284,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       umma::fence_after_sync();
       const int tt = r & 63;
       const float2 me = sc.g[tt];
-      const float mul = w < 2 ? sc.be[tt].x : a.out_scale;
+      const float mul = w < 2 ? sc.be[tt] : a.out_scale;
       const int top = w < 2 ? tt - 1 : tt;         // last column of this row
 #pragma unroll
       for (int cb = 0; cb < 4; ++cb) {
@@ -378,18 +413,25 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       }
       __syncwarp();
     };
-    auto state_product = [&](uint32_t d, uint32_t tile, uint64_t *done) {   // S (rows of tile)^T
+    // S (rows of tile)^T over half of the columns: 32 from either half of the chain
+    auto state_product = [&](uint32_t d, uint32_t tile, int half) {
       if (elect_one()) {
 #pragma unroll
         for (int p = 2; p >= 0; --p)
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ts(tm + d, tm + kTmS + p * 64 + k * 8, kmaj(tile, k), idesc(128, kT, false, false), p < 2 || k > 0);
-        umma::commit(done);
+          for (int k = 0; k < 4; ++k) {
+            const int kk = (k & 1) + 4 * (k >> 1) + 2 * half;
+            mma_ts(tm + d, tm + kTmS + p * 64 + kk * 8, kmaj(tile, kk), idesc(128, kT, false, false),
+                   half > 0 || p < 2 || k > 0);
+          }
       }
       __syncwarp();
     };
-    auto pair_product = [&](uint32_t parts, uint32_t tile, uint64_t *done) {   // into U's place
+    auto done = [&](uint64_t *b) {
+      if (elect_one()) umma::commit(b);
+      __syncwarp();
+    };
+    auto pair_product = [&](uint32_t parts, uint32_t tile, uint64_t *b) {   // into U's place
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < 6; ++c)
@@ -397,7 +439,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
           for (int k = 0; k < 4; ++k)
             mma_ts(tm + kTmU, tm + parts + kPa[c] * 32 + k * 8, desc_sw128(tile + kPb[c] * kPart + k * 32, 16),
                    idesc(128, kT, false, false), c + k > 0);
-        umma::commit(done);
+        umma::commit(b);
       }
       __syncwarp();
     };
@@ -407,9 +449,13 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     for (int i = 0; good && i < chunks; ++i) {
       const uint32_t ph = i & 1;
       const uint32_t kq = base + kOffKQ + (i & 1) * 2 * kBlk;
-      if (!warp_wait(bar + kSp, ph, abort, lim)) break;
+      if (!warp_wait(bar + kSp0, ph, abort, lim)) break;
       umma::fence_after_sync();
-      state_product(kTmU, kq, bar + kU);
+      state_product(kTmU, kq, 0);
+      if (!warp_wait(bar + kSp1, ph, abort, lim)) break;
+      umma::fence_after_sync();
+      state_product(kTmU, kq, 1);
+      done(bar + kU);
       if (!warp_wait(bar + kTm, ph, abort, lim)) break;
       if (i + 1 < chunks) {   // while the chain makes R
         if (!warp_wait(bar + kFull0 + ((i + 1) & 1), ((i + 1) >> 1) & 1, abort, lim)) break;
@@ -419,7 +465,9 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       if (!warp_wait(bar + kRp, ph, abort, lim)) break;
       umma::fence_after_sync();
       pair_product(kTmR, base + kOffT + (i & 1) * 3 * kPart, bar + kW);
-      state_product(kTmZ, kq + kPart, bar + kQ);   // while the chain splits W
+      state_product(kTmZ, kq + kPart, 0);   // while the chain splits W
+      state_product(kTmZ, kq + kPart, 1);
+      done(bar + kQ);
       if (!warp_wait(bar + kWp, ph, abort, lim)) break;
       umma::fence_after_sync();
       pair_product(kTmW, base + kOffM + (i & 1) * 3 * kPart, bar + kO);
@@ -471,7 +519,10 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
         const double G = g[k] + before;
         const float hi = (float)G;
         sc.g[lane * 2 + k] = make_float2(hi, (float)(G - (double)hi));
-        sc.be[lane * 2 + k] = make_float2(be[k], ex2((float)G));
+        const float e = ex2((float)G);
+        sc.be[lane * 2 + k] = be[k];
+        sc.bg[lane * 2 + k] = be[k] * e;
+        sc.zg[lane * 2 + k] = a.out_scale * e;
         sc.fw[lane * 2 + k] = ex2((float)(last - G));
         al[k] = aln[k];
         be[k] = ben[k];
