@@ -66,13 +66,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float x0, float x1) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(x0, x1);
   return *reinterpret_cast<const uint32_t *>(&v);
 }
+// (x0, x1) - (h0, h1), one packed instruction (exact here: h is x rounded).
+__device__ __forceinline__ void sub2(float &x0, float &x1, float h0, float h1) {
+  asm("{\n\t.reg .b64 x, h, m;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 h, {%2, %3};\n\tmov.b64 m, {%4, %4};\n\t"
+      "fma.rn.f32x2 x, h, m, x;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(h0), "f"(h1), "f"(-1.0f));
+}
 __device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
   hi = pack_bf16(x0, x1);
-  x0 -= __uint_as_float(hi << 16);
-  x1 -= __uint_as_float(hi & 0xFFFF0000u);
+  sub2(x0, x1, __uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u));
   mid = pack_bf16(x0, x1);
-  x0 -= __uint_as_float(mid << 16);
-  x1 -= __uint_as_float(mid & 0xFFFF0000u);
+  sub2(x0, x1, __uint_as_float(mid << 16), __uint_as_float(mid & 0xFFFF0000u));
   lo = pack_bf16(x0, x1);
 }
 
@@ -113,6 +120,14 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
+}
+
+// Registers per thread of the calling warpgroup (all of its warps call).
+template <int N> __device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Every lane of the warp arrives through lane 0, its writes before it.

@@ -20,9 +20,9 @@
 //
 // Bound by the chain S -> U -> R -> W -> S' of one chunk after the other.
 //
-// Roles: warps 0-7 the chain and the outputs (one value row per lane, two halves of the
-// columns), warps 8-11 A, M and T, warp 12 issues the products, warp 13 the
-// decays, warps 14-15 load the tiles with zeros behind the sequence's end.
+// Roles: warps 0-7 the chain (one value row per lane, two halves of the columns),
+// warps 8-11 and 12-15 A, M, T and the outputs of every second chunk, warp 16 issues
+// the products, warp 17 the decays, warps 18-19 load the tiles with zeros behind the sequence's end.
 #include "chunk.cuh"
 #include "rssm_prefill.h"
 
@@ -35,18 +35,22 @@ constexpr int kT = 64;                      // tokens per chunk
 constexpr int kD = 128;
 constexpr int kBlk = 16384;                 // 128 rows x 64 bf16
 constexpr int kPart = 8192;                 // 64 x 64 bf16
-constexpr int kThreadsG = 512;
+constexpr int kThreadsG = 640;
+// registers per thread: 256 x 120 + 256 x 88 + 128 x 64 = 640 x 96
+constexpr int kRegsLaunch = 96, kRegsChain = 120, kRegsIntra = 88, kRegsRest = 64;
+static_assert(256 * kRegsChain + 256 * kRegsIntra + 128 * kRegsRest <= kThreadsG * kRegsLaunch, "registers of the CTA");
 constexpr int kALd = 68, kTLd = 36, kXLd = 20;   // floats per row of A^T, of 32-wide and of 16-wide blocks
 // shared memory
 constexpr int kOffKQ = 0;                   // two stages: rows 0-63 K, 64-127 Q, two column blocks
 constexpr int kOffV = 4 * kBlk;             // two stages [t][dv]
 constexpr int kOffT = kOffV + 2 * kBlk;     // two buffers of three parts, [t][s]
 constexpr int kOffM = kOffT + 6 * kPart;
-constexpr int kOffA = kOffM + 6 * kPart;    // A^T in fp32, [s][t]
-constexpr int kOffTa = kOffA + kT * kALd * 4;      // T's first 32 rows and columns, [row][column]
-constexpr int kOffTb = kOffTa + 32 * kTLd * 4;     // its last 32, [column][row]
-constexpr int kOffX = kOffTb + 32 * kTLd * 4;      // blocks on the way
-constexpr int kOffSc = kOffX + 4 * 16 * kXLd * 4;
+constexpr int kOffTa = kOffM + 6 * kPart;          // two of: T's first 32 rows and columns, [row][column]
+constexpr int kOffTb = kOffTa + 32 * kTLd * 4;     //   its last 32, [column][row]
+constexpr int kOffX = kOffTb + 32 * kTLd * 4;      //   blocks on the way
+constexpr int kScratch = 2 * 32 * kTLd * 4 + 4 * 16 * kXLd * 4;
+constexpr int kOffSc = kOffTa + 2 * kScratch;
+static_assert(kT * kALd * 4 <= 3 * kPart, "A^T (fp32, [s][t]) lies where T's parts go");
 struct Scalars {
   float2 g[kT];        // G as two floats, in powers of two
   float be[kT];        // b_t
@@ -56,8 +60,8 @@ struct Scalars {
   float last, pad[3];  // e^{G_last}
 };
 constexpr int kOffBar = kOffSc + 2 * (int)sizeof(Scalars);
-enum { kFull0 = 0, kFull1, kStage0, kStage1, kScFull0, kScFull1, kScFree0, kScFree1, kA, kTm, kSp0, kSp1, kU, kQ, kRp, kW,
-       kWp, kFwp, kO, kUpd, kDrain, kBars };
+enum { kFull0 = 0, kFull1, kStage0, kStage1, kScFull0, kScFull1, kScFree0, kScFree1, kA0, kA1, kTm0, kTm1, kO0, kO1,
+       kSp0, kSp1, kU, kQ, kRp, kW, kWp, kFwp, kUpd, kOfree, kAfree, kDrain, kBars };
 constexpr int kSmemG = kOffBar + kBars * 8 + 32;
 static_assert(kSmemG <= 232448 && 32 * kTLd <= 4 * 16 * kXLd, "shared memory of one CTA");
 // tensor memory columns.  U^T, then W^T, then the masked product; Z^T; the parts of S,
@@ -110,12 +114,12 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
   Scalars *scs = reinterpret_cast<Scalars *>(smem + kOffSc);
   const uint32_t base = smem_u32(smem);
   if (t == 0) {
-    const int count[kBars] = {64, 64, 1, 1, 1, 1, 12, 12, 1, 4, 8, 8, 1, 1, 8, 1, 8, 8, 1, 1, 1};
+    const int count[kBars] = {64, 64, 1, 1, 1, 1, 12, 12, 1, 1, 4, 4, 1, 1, 8, 8, 1, 1, 8, 1, 8, 8, 1, 4, 4, 1};
     for (int i = 0; i < kBars; ++i) mbar_init(bar + i, count[i]);
     *abort = 0;
     mbar_fence_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     umma::alloc(tm_slot, 512);
     umma::relinquish();
   }
@@ -130,6 +134,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
 
   if (warp < 8) {
     // -------------------------------------------------------- the chain
+    more_registers<kRegsChain>();
     const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
     float S[64];
@@ -220,31 +225,6 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       wait_st();
       umma::fence_before_sync();
       warp_arrive(bar + kFwp);
-      good = warp_wait(bar + kO, ph, abort, lim);
-      if (!good) break;
-      umma::fence_after_sync();
-      {   // the outputs of this half's tokens, a value row per lane
-        const int left = q.n - i * kT - wg * 32;
-        float *o = a.out + ((size_t)(q.tok + i * kT + wg * 32) * a.H + h) * kD + row;
-        const size_t step = (size_t)a.H * kD;
-#pragma unroll
-        for (int c = 0; c < 32; c += 16) {
-          float u[16], z[16];
-          umma::ld_32x32b_x16(lanes + kTmU + wg * 32 + c, u);
-          umma::ld_32x32b_x16(lanes + kTmZ + wg * 32 + c, z);
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 g = *reinterpret_cast<const float4 *>(&sc.zg[wg * 32 + c + j]);
-            u[j] = fmaf(g.x, z[j], u[j]);
-            u[j + 1] = fmaf(g.y, z[j + 1], u[j + 1]);
-            u[j + 2] = fmaf(g.z, z[j + 2], u[j + 2]);
-            u[j + 3] = fmaf(g.w, z[j + 3], u[j + 3]);
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < left) __stcs(o + (c + j) * step, u[j]);
-        }
-      }
       const float dec = sc.last;
       warp_arrive(bar + kScFree0 + (i & 1));
       good = warp_wait(bar + kUpd, ph, abort, lim);
@@ -268,19 +248,23 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
 #pragma unroll
       for (int c = 0; c < 64; c += 8) st_sector(dst + c, S + c);
     }
-  } else if (warp < 12) {
-    // -------------------------------------------------------- A, M and T
-    const int w = warp - 8, r = w * 32 + lane;
+  } else if (warp < 16) {
+    // ------------------------------- A, M, T and the outputs of every second chunk
+    fewer_registers<kRegsIntra>();
+    const int me4 = (warp - 8) >> 2, w = warp & 3, r = w * 32 + lane;
+    const int sync_all = 1 + me4 * 3;   // named barriers of this warpgroup
     const uint32_t lanes = tm + ((uint32_t)(w * 32) << 16);
-    float *sA = reinterpret_cast<float *>(smem + kOffA), *sTa = reinterpret_cast<float *>(smem + kOffTa);
-    float *sTb = reinterpret_cast<float *>(smem + kOffTb), *sX = reinterpret_cast<float *>(smem + kOffX);
-    for (int i = 0; i < chunks; ++i) {
-      const int buf = i & 1;
+    float *sA = reinterpret_cast<float *>(smem + kOffT + me4 * 3 * kPart);
+    float *sTa = reinterpret_cast<float *>(smem + kOffTa + me4 * kScratch);
+    float *sTb = reinterpret_cast<float *>(smem + kOffTb + me4 * kScratch);
+    float *sX = reinterpret_cast<float *>(smem + kOffX + me4 * kScratch);
+    for (int i = me4; i < chunks; i += 2) {
+      const int buf = me4;
       const Scalars &sc = scs[buf];
       const bool ok = warp_wait(bar + kScFull0 + buf, (i >> 1) & 1, abort, lim) &&
-                      warp_wait(bar + kA, i & 1, abort, lim) &&
+                      warp_wait(bar + kA0 + buf, (i >> 1) & 1, abort, lim) &&
                       (i < 2 || warp_wait(bar + kStage0 + buf, ((i >> 1) - 1) & 1, abort, lim));   // T and M are read
-      if (named_sync_or(1, 128, !ok)) break;   // the four warps agree; the chunk before's blocks are read
+      if (named_sync_or(sync_all, 128, !ok)) break;   // the four warps agree; the chunk before's blocks are read
       umma::fence_after_sync();
       const int tt = r & 63;
       const float2 me = sc.g[tt];
@@ -313,8 +297,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
         }
       }
       umma::fence_before_sync();
-      named_sync(1, 128);
-      warp_arrive(bar + kScFree0 + buf);
+      warp_arrive(bar + kAfree);
+      named_sync(sync_all, 128);
       // T by blocks.  Sixteen-wide diagonal blocks by substitution, one per warp, a column per
       // lane; then T_10 = -T_11 (A_10 T_00) for pairs of blocks, and again for pairs of those.
       {
@@ -349,7 +333,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
           }
         }
       }
-      named_sync(1, 128);
+      named_sync(sync_all, 128);
       {
         const int pr = w >> 1, id = r & 63, c = id & 15, r4 = (id >> 4) * 4;
         float x[4][1];
@@ -358,7 +342,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
                          pr ? kXLd : kTLd, 16);
 #pragma unroll
         for (int e = 0; e < 4; ++e) sXp[(r4 + e) * kXLd + c] = x[e][0];
-        named_sync(2 + pr, 64);
+        named_sync(sync_all + 1 + pr, 64);
         block_product<1>(x, pr ? sTb + 16 * kTLd + 16 + r4 : sX + r4, pr ? kTLd : kXLd, sXp + c, kXLd, 16);
         if (pr) {
           *reinterpret_cast<float4 *>(sTb + c * kTLd + 16 + r4) = make_float4(-x[0][0], -x[1][0], -x[2][0], -x[3][0]);
@@ -367,7 +351,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
           for (int e = 0; e < 4; ++e) sTa[(16 + r4 + e) * kTLd + c] = -x[e][0];
         }
       }
-      named_sync(1, 128);
+      named_sync(sync_all, 128);
       {
         const int c = (r & 15) * 2, r4 = (r >> 4) * 4;
         auto put = [&](int row, int col, float v0, float v1) {
@@ -382,6 +366,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
         block_product<2>(x, sA + 32 + r4, kALd, sTa + c, kTLd, 32);
 #pragma unroll
         for (int e = 0; e < 4; ++e) *reinterpret_cast<float2 *>(sX + (r4 + e) * kTLd + c) = make_float2(x[e][0], x[e][1]);
+        named_sync(sync_all, 128);   // A is read: its place takes T's parts
+        block_product<2>(x, sTb + r4, kTLd, sX + c, kTLd, 32);
         const float4 b0 = *reinterpret_cast<const float4 *>(sTb + c * kTLd + r4);
         const float4 b1 = *reinterpret_cast<const float4 *>(sTb + (c + 1) * kTLd + r4);
         const float y0[4] = {b0.x, b0.y, b0.z, b0.w}, y1[4] = {b1.x, b1.y, b1.z, b1.w};
@@ -389,18 +375,52 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
         for (int e = 0; e < 4; ++e) {
           const float2 v = *reinterpret_cast<const float2 *>(sTa + (r4 + e) * kTLd + c);
           put(r4 + e, c, v.x, v.y);
+          put(r4 + e, 32 + c, 0.f, 0.f);
           put(32 + r4 + e, 32 + c, y0[e], y1[e]);
         }
-        named_sync(1, 128);
-        block_product<2>(x, sTb + r4, kTLd, sX + c, kTLd, 32);
+
 #pragma unroll
         for (int e = 0; e < 4; ++e) put(32 + r4 + e, c, -x[e][0], -x[e][1]);
       }
       fence_proxy_async();
-      warp_arrive(bar + kTm);
+      warp_arrive(bar + kTm0 + buf);
+      // the chunk's outputs, a value row per lane (a give-up is agreed on at the loop's head)
+      if (!warp_wait(bar + kO0 + buf, (i >> 1) & 1, abort, lim)) continue;
+      umma::fence_after_sync();
+      const int left = q.n - i * kT;
+      const size_t step = (size_t)a.H * kD;
+      float *o = a.out + ((size_t)(q.tok + i * kT) * a.H + h) * kD + r;
+#pragma unroll
+      for (int c = 0; c < kT; c += 16) {
+        float u[16], z[16];
+        umma::ld_32x32b_x16(lanes + kTmU + c, u);
+        umma::ld_32x32b_x16(lanes + kTmZ + c, z);
+        if (c + 16 == kT) {
+          umma::fence_before_sync();
+          warp_arrive(bar + kOfree);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 g = *reinterpret_cast<const float4 *>(&sc.zg[c + j]);
+          u[j] = fmaf(g.x, z[j], u[j]);
+          u[j + 1] = fmaf(g.y, z[j + 1], u[j + 1]);
+          u[j + 2] = fmaf(g.z, z[j + 2], u[j + 2]);
+          u[j + 3] = fmaf(g.w, z[j + 3], u[j + 3]);
+        }
+        if (left >= kT) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j, o += step) __stcs(o, u[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j, o += step)
+            if (c + j < left) __stcs(o, u[j]);
+        }
+      }
+      warp_arrive(bar + kScFree0 + buf);
     }
-  } else if (warp == 12) {
+  } else if (warp == 16) {
     // -------------------------------------------------------- the products
+    fewer_registers<kRegsRest>();
     auto kmaj = [](uint32_t tile, int k) { return desc_sw128(tile + (k / 4) * kBlk + (k % 4) * 32, 16); };
     auto mnmaj = [](uint32_t tile, int k) { return desc_sw128(tile + k * 2048, kBlk); };
     auto gram = [&](int i) {   // [K; Q] K^T
@@ -409,7 +429,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           umma::mma_bf16(tm + kTmA, kmaj(kq, k), kmaj(kq, k), idesc(128, kT, false, false), k > 0);
-        umma::commit(bar + kA);
+        umma::commit(bar + kA0 + (i & 1));
       }
       __syncwarp();
     };
@@ -450,18 +470,20 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       const uint32_t ph = i & 1;
       const uint32_t kq = base + kOffKQ + (i & 1) * 2 * kBlk;
       if (!warp_wait(bar + kSp0, ph, abort, lim)) break;
+      if (i > 0 && !warp_wait(bar + kOfree, ph ^ 1, abort, lim)) break;
       umma::fence_after_sync();
       state_product(kTmU, kq, 0);
       if (!warp_wait(bar + kSp1, ph, abort, lim)) break;
       umma::fence_after_sync();
       state_product(kTmU, kq, 1);
       done(bar + kU);
-      if (!warp_wait(bar + kTm, ph, abort, lim)) break;
       if (i + 1 < chunks) {   // while the chain makes R
+        if (!warp_wait(bar + kAfree, ph, abort, lim)) break;
         if (!warp_wait(bar + kFull0 + ((i + 1) & 1), ((i + 1) >> 1) & 1, abort, lim)) break;
         umma::fence_after_sync();
         gram(i + 1);
       }
+      if (!warp_wait(bar + kTm0 + (i & 1), (i >> 1) & 1, abort, lim)) break;
       if (!warp_wait(bar + kRp, ph, abort, lim)) break;
       umma::fence_after_sync();
       pair_product(kTmR, base + kOffT + (i & 1) * 3 * kPart, bar + kW);
@@ -470,7 +492,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       done(bar + kQ);
       if (!warp_wait(bar + kWp, ph, abort, lim)) break;
       umma::fence_after_sync();
-      pair_product(kTmW, base + kOffM + (i & 1) * 3 * kPart, bar + kO);
+      pair_product(kTmW, base + kOffM + (i & 1) * 3 * kPart, bar + kO0 + (i & 1));
       if (!warp_wait(bar + kFwp, ph, abort, lim)) break;
       umma::fence_after_sync();
       if (elect_one()) {
@@ -484,8 +506,9 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       }
       __syncwarp();
     }
-  } else if (warp == 13) {
+  } else if (warp == 17) {
     // -------------------------------------------------------- decays
+    fewer_registers<kRegsRest>();
     const float *pa = static_cast<const float *>(a.in[3]) + h, *pb = static_cast<const float *>(a.in[4]) + h;
     auto load = [&](int i, float (&al)[2], float (&be)[2]) {
 #pragma unroll
@@ -532,7 +555,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     }
   } else {
     // -------------------------------------------------------- tiles
-    const int l = t - 448;   // 0..63
+    fewer_registers<kRegsRest>();
+    const int l = t - 576;   // 0..63
     const __nv_bfloat16 *in[3];
 #pragma unroll
     for (int k = 0; k < 3; ++k) in[k] = static_cast<const __nv_bfloat16 *>(a.in[k]) + (size_t)h * kD;
@@ -561,7 +585,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  if (warp == 12) {
+  if (warp == 16) {
     if (*abort) {   // products may still be in flight: wait for them before their memory goes
       if (lane == 0) {
         umma::commit(bar + kDrain);
