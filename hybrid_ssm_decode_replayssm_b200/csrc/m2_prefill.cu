@@ -19,9 +19,9 @@
 // barrier can complete again before all its waiters have passed: full -> stage freed
 // by y, CB -> L, inter -> y, upd -> the next fw x, decays -> both users.
 //
-// Roles: warps 0-3 (one token per lane) make L from CB and write y; warps 4-7 (one n
-// per lane) make fw x, update the state and split it; warp 8 issues the products;
-// warp 9 computes the decays; warps 10-13 load the tiles with zeros behind the
+// Roles: warps 0-7 (one token per lane, two halves of the columns) make L from CB and
+// write y; warps 8-11 (one n per lane) make fw x, update the state and split it; warp
+// 12 issues the products; warp 13 computes the decays; warps 14-17 load the tiles with zeros behind the
 // sequence's end, so that nothing past it is ever read.
 #include "chunk.cuh"
 #include "rssm_prefill.h"
@@ -34,7 +34,7 @@ using namespace chunk;
 constexpr int kT = 128;                // tokens per chunk
 constexpr int kP = 64;
 constexpr int kBlk = 16384;            // 128 rows x 64 bf16
-constexpr int kWarpsM = 14;
+constexpr int kWarpsM = 18;
 constexpr int kThreadsM = kWarpsM * 32;
 // shared memory
 constexpr int kOffB = 0;               // two stages of B, two 64-column blocks each
@@ -44,7 +44,7 @@ constexpr int kOffH = 8 * kBlk;        // three parts of the state, [n][p]
 constexpr int kOffXp = 11 * kBlk;      // three parts of fw x, [s][p]
 constexpr int kOffSc = 14 * kBlk;      // float4 (G hi, G lo, dt, fw) per token
 constexpr int kOffBar = kOffSc + kT * 16;
-enum { kFull0 = 0, kFull1, kCb, kInter, kUpd, kIntra, kL, kHp, kXp, kYfree, kScFull, kScFree, kStage0, kStage1,
+enum { kFull0 = 0, kFull1, kCb, kInter, kUpd, kIntra, kL0, kL1, kHp, kXp, kYfree, kScFull, kScFree, kStage0, kStage1,
        kDrain, kBars };
 constexpr int kSmemM = kOffBar + kBars * 8 + 32;
 static_assert(kSmemM <= 232448, "shared memory of one CTA");
@@ -66,12 +66,12 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
   float4 *sc = reinterpret_cast<float4 *>(smem + kOffSc);
   const uint32_t base = smem_u32(smem);
   if (t == 0) {
-    const int count[kBars] = {128, 128, 1, 1, 1, 1, 4, 4, 4, 4, 1, 8, 4, 4, 1};
+    const int count[kBars] = {128, 128, 1, 1, 1, 1, 8, 8, 4, 4, 8, 1, 12, 8, 8, 1};
     for (int i = 0; i < kBars; ++i) mbar_init(bar + i, count[i]);
     *abort = 0;
     mbar_fence_init();
   }
-  if (warp == 8) {
+  if (warp == 12) {
     umma::alloc(tm_slot, 512);
     umma::relinquish();
   }
@@ -92,85 +92,76 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
   const float *src = a.hc + ((size_t)(q.src < 0 ? 0 : q.src) * a.H + h) * kP * N;
   float *dst = a.hc + ((size_t)q.dst * a.H + h) * kP * N;
 
-  if (warp < 4) {
+  if (warp < 8) {
     // ------------------------------------------------ L, and the outputs
-    const uint32_t lanes = tm + ((uint32_t)(warp * 32) << 16);
-    uint32_t z[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) z[j] = 0u;
-    for (int cb = warp + 1; cb < 4; ++cb)   // above the diagonal L stays zero
-      for (int p = 0; p < 3; ++p) st_x16(lanes + kTmL + p * 64 + cb * 16, z);
+    // two warps per 32 tokens: each takes sixteen of every 32 columns of L, and half of y
+    const int wg = warp >> 2, w = warp & 3, row = w * 32 + lane;
+    const uint32_t lanes = tm + ((uint32_t)(w * 32) << 16);
+    {
+      const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      for (int cb = w + 1; cb < 4; ++cb)   // above the diagonal L stays zero
+        for (int p = 0; p < 3; ++p) st_x8(lanes + kTmL + p * 64 + cb * 16 + wg * 8, z);
+    }
     const float Dh = __ldg(a.D + h);
     for (int i = 0; i < chunks; ++i) {
       const uint32_t ph = i & 1;
       if (!warp_wait(bar + kScFull, ph, abort, lim) || !warp_wait(bar + kCb, ph, abort, lim)) break;
       umma::fence_after_sync();
-      const float4 me = sc[t];
-      for (int cb = 0; cb <= warp; ++cb) {
-        float v[32];
-        umma::ld_32x32b_x32(lanes + kTmCb + cb * 32, v);
-        uint32_t hi[16], mid[16], lo[16];
+      const float4 me = sc[row];
+      for (int cb = 0; cb < 4; ++cb) {
+        if (cb <= w) {
+          float v[16];
+          umma::ld_32x32b_x16(lanes + kTmCb + cb * 32 + wg * 16, v);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float4 s0 = sc[cb * 32 + j], s1 = sc[cb * 32 + j + 1];
-          float e0 = ex2((me.x - s0.x) + (me.y - s0.y)) * (s0.z * v[j]);
-          float e1 = ex2((me.x - s1.x) + (me.y - s1.y)) * (s1.z * v[j + 1]);
-          if (cb == warp) {
-            e0 = j <= lane ? e0 : 0.f;
-            e1 = j + 1 <= lane ? e1 : 0.f;
+          for (int j = 0; j < 16; ++j) {
+            const float4 s = sc[cb * 32 + wg * 16 + j];
+            v[j] = ex2((me.x - s.x) + (me.y - s.y)) * (s.z * v[j]);
+            if (cb == w) v[j] = wg * 16 + j <= lane ? v[j] : 0.f;
           }
-          split3(e0, e1, hi[j / 2], mid[j / 2], lo[j / 2]);
+          split_store(lanes + kTmL + cb * 16 + wg * 8, 64, v);
         }
-        st_x16(lanes + kTmL + cb * 16, hi);
-        st_x16(lanes + kTmL + 64 + cb * 16, mid);
-        st_x16(lanes + kTmL + 128 + cb * 16, lo);
+        if (cb & 1) {   // the product can start on half of the columns
+          wait_st();
+          umma::fence_before_sync();
+          warp_arrive(bar + kL0 + (cb >> 1));
+        }
       }
-      wait_st();
-      umma::fence_before_sync();
-      warp_arrive(bar + kL);
       warp_arrive(bar + kScFree);
       if (!warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim) || !warp_wait(bar + kInter, ph, abort, lim)) break;
       umma::fence_after_sync();
       const float g = ex2(me.x + me.y);
       const uint8_t *xrow = smem + kOffX + (i & 1) * kBlk;
-      float y[kP];
+      float y[32];
+      umma::ld_32x32b_x32(lanes + kTmInter + wg * 32, y);
 #pragma unroll
-      for (int c = 0; c < kP; c += 32) {
-        float v[32];
-        umma::ld_32x32b_x32(lanes + kTmInter + c, v);
+      for (int j = 0; j < 32; j += 8) {
+        const uint4 raw = *reinterpret_cast<const uint4 *>(xrow + sw128(row, wg * 4 + j / 8));
+        const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          const uint4 raw = *reinterpret_cast<const uint4 *>(xrow + sw128(t, (c + j) / 8));
-          const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            y[c + j + 2 * k] = fmaf(g, v[j + 2 * k], Dh * __uint_as_float(w[k] << 16));
-            y[c + j + 2 * k + 1] = fmaf(g, v[j + 2 * k + 1], Dh * __uint_as_float(w[k] & 0xFFFF0000u));
-          }
+        for (int k = 0; k < 4; ++k) {
+          y[j + 2 * k] = fmaf(g, y[j + 2 * k], Dh * __uint_as_float(x[k] << 16));
+          y[j + 2 * k + 1] = fmaf(g, y[j + 2 * k + 1], Dh * __uint_as_float(x[k] & 0xFFFF0000u));
         }
       }
       if (!warp_wait(bar + kIntra, ph, abort, lim)) break;
       umma::fence_after_sync();
-#pragma unroll
-      for (int c = 0; c < kP; c += 32) {
-        float v[32];
-        umma::ld_32x32b_x32(lanes + kTmIntra + c, v);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) y[c + j] += v[j];
-      }
+      float v[32];
+      umma::ld_32x32b_x32(lanes + kTmIntra + wg * 32, v);
       umma::fence_before_sync();
       warp_arrive(bar + kYfree);
       warp_arrive(bar + kStage0 + (i & 1));
-      if (i * kT + t < q.n) {
-        float *o = a.out + ((size_t)(q.tok + i * kT + t) * a.H + h) * kP;
 #pragma unroll
-        for (int c = 0; c < kP; c += 8) st_sector(o + c, y + c);
+      for (int j = 0; j < 32; ++j) y[j] += v[j];
+      if (i * kT + row < q.n) {
+        float *o = a.out + ((size_t)(q.tok + i * kT + row) * a.H + h) * kP + wg * 32;
+#pragma unroll
+        for (int c = 0; c < 32; c += 8) st_sector(o + c, y + c);
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     // ------------------------------------------------ the state
-    const int n = t - 128;
-    const uint32_t lanes = tm + ((uint32_t)((warp - 4) * 32) << 16);
+    const int n = t - 256;
+    const uint32_t lanes = tm + ((uint32_t)((warp - 8) * 32) << 16);
     float S[kP];
 #pragma unroll
     for (int p = 0; p < kP; ++p) S[p] = q.src < 0 || n >= N ? 0.f : __ldcs(src + (size_t)p * N + n);
@@ -182,13 +173,18 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
 #pragma unroll
       for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4 *>(smem + part_off + p * kBlk + sw128(row, c16)) = w[p];
     };
-    bool good = true;
-    for (int i = 0; i < chunks; ++i) {
-      const uint32_t ph = i & 1;
-#pragma unroll
-      for (int c = 0; c < kP; c += 8) put(kOffH, n, S + c, c / 8);
+    auto state_ready = [&]() {
       fence_proxy_async();
       warp_arrive(bar + kHp);
+    };
+    bool good = true;
+    if (chunks > 0) {
+#pragma unroll
+      for (int c = 0; c < kP; c += 8) put(kOffH, n, S + c, c / 8);
+      state_ready();
+    }
+    for (int i = 0; i < chunks; ++i) {
+      const uint32_t ph = i & 1;
       good = warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim) && warp_wait(bar + kScFull, ph, abort, lim);
       if (!good) break;
       const float dec = *s_last;
@@ -213,21 +209,29 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       good = warp_wait(bar + kUpd, ph, abort, lim);
       if (!good) break;
       umma::fence_after_sync();
+      const bool more = i + 1 < chunks;
 #pragma unroll
-      for (int c = 0; c < kP; c += 32) {
-        float v[32];
-        umma::ld_32x32b_x32(lanes + kTmU + c, v);
+      for (int c = 0; c < kP; c += 16) {
+        float v[16];
+        umma::ld_32x32b_x16(lanes + kTmU + c, v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[c + j] = fmaf(dec, S[c + j], v[j]);
+        for (int j = 0; j < 16; ++j) S[c + j] = fmaf(dec, S[c + j], v[j]);
+        if (more) {
+          put(kOffH, n, S + c, c / 8);
+          put(kOffH, n, S + c + 8, c / 8 + 1);
+        }
       }
       umma::fence_before_sync();
+      if (more) state_ready();
     }
     if (good && n < N)
 #pragma unroll
       for (int p = 0; p < kP; ++p) dst[(size_t)p * N + n] = S[p];
-  } else if (warp == 8) {
+  } else if (warp == 12) {
     // ------------------------------------------------ the products
     constexpr int KN = N / 16;   // K steps along n
+    // sums run from the small parts of a split to the large: the tensor core truncates
+    // each addition, and only those of the last, large part then count
     for (int i = 0; i < chunks; ++i) {
       const uint32_t ph = i & 1;
       const uint32_t Bt = base + kOffB + (i & 1) * 2 * kBlk, Ct = base + kOffC, Xt = base + kOffX + (i & 1) * kBlk;
@@ -235,7 +239,8 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       auto mnmaj = [](uint32_t tile, int k) { return desc_sw128(tile + k * 2048, kBlk); };
       if (!warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim)) break;
       umma::fence_after_sync();
-      if (lane == 0) {
+      if (elect_one()) {
+#pragma unroll
         for (int k = 0; k < KN; ++k)
           umma::mma_bf16(tm + kTmCb, kmaj(Ct, k), kmaj(Bt, k), idesc(128, 128, false, false), k > 0);
         umma::commit(bar + kCb);
@@ -244,35 +249,49 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       if (!warp_wait(bar + kHp, ph, abort, lim)) break;
       if (i > 0 && !warp_wait(bar + kYfree, ph ^ 1, abort, lim)) break;
       umma::fence_after_sync();
-      if (lane == 0) {
-        for (int p = 0; p < 3; ++p)
+      if (elect_one()) {
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
           for (int k = 0; k < KN; ++k)
             umma::mma_bf16(tm + kTmInter, kmaj(Ct, k), mnmaj(base + kOffH + p * kBlk, k), idesc(128, kP, false, true),
-                           p + k > 0);
+                           p < 2 || k > 0);
         umma::commit(bar + kInter);
       }
       __syncwarp();
       if (!warp_wait(bar + kXp, ph, abort, lim)) break;
       umma::fence_after_sync();
-      if (lane == 0) {
-        for (int p = 0; p < 3; ++p)
+      if (elect_one()) {
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
           for (int k = 0; k < kT / 16; ++k)
             umma::mma_bf16(tm + kTmU, mnmaj(Bt, k), mnmaj(base + kOffXp + p * kBlk, k), idesc(128, kP, true, true),
-                           p + k > 0);
+                           p < 2 || k > 0);
         umma::commit(bar + kUpd);
       }
       __syncwarp();
-      if (!warp_wait(bar + kL, ph, abort, lim)) break;
-      umma::fence_after_sync();
-      if (lane == 0) {
-        for (int p = 0; p < 3; ++p)
-          for (int k = 0; k < kT / 16; ++k)
-            mma_ts(tm + kTmIntra, tm + kTmL + p * 64 + k * 8, mnmaj(Xt, k), idesc(128, kP, false, true), p + k > 0);
-        umma::commit(bar + kIntra);
+      bool ok = true;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        ok = ok && warp_wait(bar + kL0 + half, ph, abort, lim);
+        if (!ok) break;
+        umma::fence_after_sync();
+        if (elect_one()) {
+#pragma unroll
+          for (int p = 2; p >= 0; --p)
+#pragma unroll
+            for (int k = half * 4; k < half * 4 + 4; ++k)
+              mma_ts(tm + kTmIntra, tm + kTmL + p * 64 + k * 8, mnmaj(Xt, k), idesc(128, kP, false, true),
+                     half > 0 || p < 2 || k > 0);
+        }
+        __syncwarp();
       }
+      if (!ok) break;
+      if (elect_one()) umma::commit(bar + kIntra);
       __syncwarp();
     }
-  } else if (warp == 9) {
+  } else if (warp == 13) {
     // ------------------------------------------------ decays
     const double Ah = (double)__ldg(a.A + h) * 1.4426950408889634;   // in powers of two
     const __nv_bfloat16 *pdt = static_cast<const __nv_bfloat16 *>(a.in[3]) + h;
@@ -314,7 +333,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
     }
   } else {
     // ------------------------------------------------ tiles
-    const int l = t - 320;   // 0..127
+    const int l = t - 448;   // 0..127
     const int g = h / a.hpg;
     const __nv_bfloat16 *px = static_cast<const __nv_bfloat16 *>(a.in[0]) + (size_t)h * kP;
     const __nv_bfloat16 *pB = static_cast<const __nv_bfloat16 *>(a.in[1]) + (size_t)g * N;
@@ -347,7 +366,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  if (warp == 8) {
+  if (warp == 12) {
     if (*abort) {   // products may still be in flight: wait for them before their memory goes
       if (lane == 0) {
         umma::commit(bar + kDrain);
