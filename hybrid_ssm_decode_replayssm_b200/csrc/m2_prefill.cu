@@ -20,8 +20,8 @@
 // by y, CB -> L, inter -> y, upd -> the next fw x, decays -> both users.
 //
 // Roles: warps 0-7 (one token per lane, two halves of the columns) make L from CB and
-// write y; warps 8-11 (one n per lane) make fw x, update the state and split it; warp
-// 12 issues the products; warp 13 computes the decays; warps 14-17 load the tiles with zeros behind the
+// write y; warps 8-15 (one n per lane, two halves of p) make fw x, update the state and
+// split it; warp 16 issues the products; warp 17 computes the decays; warps 18-21 load the tiles with zeros behind the
 // sequence's end, so that nothing past it is ever read.
 #include "chunk.cuh"
 #include "rssm_prefill.h"
@@ -34,7 +34,7 @@ using namespace chunk;
 constexpr int kT = 128;                // tokens per chunk
 constexpr int kP = 64;
 constexpr int kBlk = 16384;            // 128 rows x 64 bf16
-constexpr int kWarpsM = 18;
+constexpr int kWarpsM = 22;
 constexpr int kThreadsM = kWarpsM * 32;
 // shared memory
 constexpr int kOffB = 0;               // two stages of B, two 64-column blocks each
@@ -42,9 +42,10 @@ constexpr int kOffC = 4 * kBlk;
 constexpr int kOffX = 6 * kBlk;        // two stages
 constexpr int kOffH = 8 * kBlk;        // three parts of the state, [n][p]
 constexpr int kOffXp = 11 * kBlk;      // three parts of fw x, [s][p]
+constexpr int kYRow = 272;             // bytes per token of the outputs on their way out
 constexpr int kOffSc = 14 * kBlk;      // float4 (G hi, G lo, dt, fw) per token
 constexpr int kOffBar = kOffSc + kT * 16;
-enum { kFull0 = 0, kFull1, kCb, kInter, kUpd, kIntra, kL0, kL1, kHp, kXp, kYfree, kScFull, kScFree, kStage0, kStage1,
+enum { kFull0 = 0, kFull1, kCb, kInter, kUpd, kIntra, kL0, kL1, kHp, kXp, kXfree, kYfree, kScFull, kScFree, kStage0, kStage1,
        kDrain, kBars };
 constexpr int kSmemM = kOffBar + kBars * 8 + 32;
 static_assert(kSmemM <= 232448, "shared memory of one CTA");
@@ -66,12 +67,12 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
   float4 *sc = reinterpret_cast<float4 *>(smem + kOffSc);
   const uint32_t base = smem_u32(smem);
   if (t == 0) {
-    const int count[kBars] = {128, 128, 1, 1, 1, 1, 8, 8, 4, 4, 8, 1, 12, 8, 8, 1};
+    const int count[kBars] = {128, 128, 1, 1, 1, 1, 8, 8, 8, 8, 8, 8, 1, 16, 8, 8, 1};
     for (int i = 0; i < kBars; ++i) mbar_init(bar + i, count[i]);
     *abort = 0;
     mbar_fence_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     umma::alloc(tm_slot, 512);
     umma::relinquish();
   }
@@ -152,26 +153,43 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       warp_arrive(bar + kStage0 + (i & 1));
 #pragma unroll
       for (int j = 0; j < 32; ++j) y[j] += v[j];
-      if (i * kT + row < q.n) {
-        float *o = a.out + ((size_t)(q.tok + i * kT + row) * a.H + h) * kP + wg * 32;
+      // y leaves through the place of fw x (read by now), four rows per store: a token per
+      // lane would touch 32 lines per store and hold up all of shared memory
+      uint8_t *stage = smem + kOffXp + w * 32 * kYRow + wg * 128;
 #pragma unroll
-        for (int c = 0; c < 32; c += 8) st_sector(o + c, y + c);
-      }
+      for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<float4 *>(stage + lane * kYRow + j * 4) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+      __syncwarp();
+      const int first = i * kT + w * 32 + (lane >> 3);
+      float *o = a.out + ((size_t)(q.tok + first) * a.H + h) * kP + wg * 32 + (lane & 7) * 4;
+      const size_t step = (size_t)4 * a.H * kP;
+      float4 z[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        z[k] = *reinterpret_cast<const float4 *>(stage + (k * 4 + (lane >> 3)) * kYRow + (lane & 7) * 16);
+#pragma unroll
+      for (int k = 0; k < 8; ++k, o += step)
+        if (first + k * 4 < q.n) st_stream(o, z[k]);
+      warp_arrive(bar + kXfree);
     }
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // ------------------------------------------------ the state
-    const int n = t - 256;
-    const uint32_t lanes = tm + ((uint32_t)((warp - 8) * 32) << 16);
-    float S[kP];
+    const int u = t - 256, wg = (warp - 8) >> 2, n = (warp & 3) * 32 + lane, p0 = wg * 32;
+    const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    float S[32];
 #pragma unroll
-    for (int p = 0; p < kP; ++p) S[p] = q.src < 0 || n >= N ? 0.f : __ldcs(src + (size_t)p * N + n);
+    for (int p = 0; p < 32; ++p) S[p] = q.src < 0 || n >= N ? 0.f : __ldcs(src + (size_t)(p0 + p) * N + n);
     auto put = [&](int part_off, int row, const float *v8, int c16) {   // 8 values -> three parts
       uint4 w[3];
-      uint32_t *u = reinterpret_cast<uint32_t *>(w);
+      uint32_t *x = reinterpret_cast<uint32_t *>(w);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) split3(v8[2 * k], v8[2 * k + 1], u[k], u[4 + k], u[8 + k]);
+      for (int k = 0; k < 4; ++k) split3(v8[2 * k], v8[2 * k + 1], x[k], x[4 + k], x[8 + k]);
 #pragma unroll
       for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4 *>(smem + part_off + p * kBlk + sw128(row, c16)) = w[p];
+    };
+    auto put_state = [&](int c) {
+      put(kOffH, n, S + c, (p0 + c) / 8);
+      put(kOffH, n, S + c + 8, (p0 + c) / 8 + 1);
     };
     auto state_ready = [&]() {
       fence_proxy_async();
@@ -179,19 +197,20 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
     };
     bool good = true;
     if (chunks > 0) {
-#pragma unroll
-      for (int c = 0; c < kP; c += 8) put(kOffH, n, S + c, c / 8);
+      put_state(0);
+      put_state(16);
       state_ready();
     }
     for (int i = 0; i < chunks; ++i) {
       const uint32_t ph = i & 1;
-      good = warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim) && warp_wait(bar + kScFull, ph, abort, lim);
+      good = warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim) && warp_wait(bar + kScFull, ph, abort, lim) &&
+             (i == 0 || warp_wait(bar + kXfree, ph ^ 1, abort, lim));
       if (!good) break;
       const float dec = *s_last;
       const uint8_t *x = smem + kOffX + (i & 1) * kBlk;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int s = k * 16 + n / 8, c16 = n % 8;
+      for (int k = 0; k < 4; ++k) {
+        const int s = k * 32 + u / 8, c16 = u % 8;
         const float fw = sc[s].w;
         const uint4 raw = *reinterpret_cast<const uint4 *>(x + sw128(s, c16));
         const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -211,23 +230,20 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       umma::fence_after_sync();
       const bool more = i + 1 < chunks;
 #pragma unroll
-      for (int c = 0; c < kP; c += 16) {
+      for (int c = 0; c < 32; c += 16) {
         float v[16];
-        umma::ld_32x32b_x16(lanes + kTmU + c, v);
+        umma::ld_32x32b_x16(lanes + kTmU + p0 + c, v);
 #pragma unroll
         for (int j = 0; j < 16; ++j) S[c + j] = fmaf(dec, S[c + j], v[j]);
-        if (more) {
-          put(kOffH, n, S + c, c / 8);
-          put(kOffH, n, S + c + 8, c / 8 + 1);
-        }
+        if (more) put_state(c);
       }
       umma::fence_before_sync();
       if (more) state_ready();
     }
     if (good && n < N)
 #pragma unroll
-      for (int p = 0; p < kP; ++p) dst[(size_t)p * N + n] = S[p];
-  } else if (warp == 12) {
+      for (int p = 0; p < 32; ++p) dst[(size_t)(p0 + p) * N + n] = S[p];
+  } else if (warp == 16) {
     // ------------------------------------------------ the products
     constexpr int KN = N / 16;   // K steps along n
     // sums run from the small parts of a split to the large: the tensor core truncates
@@ -291,7 +307,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       if (elect_one()) umma::commit(bar + kIntra);
       __syncwarp();
     }
-  } else if (warp == 13) {
+  } else if (warp == 17) {
     // ------------------------------------------------ decays
     const double Ah = (double)__ldg(a.A + h) * 1.4426950408889634;   // in powers of two
     const __nv_bfloat16 *pdt = static_cast<const __nv_bfloat16 *>(a.in[3]) + h;
@@ -333,7 +349,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
     }
   } else {
     // ------------------------------------------------ tiles
-    const int l = t - 448;   // 0..127
+    const int l = t - 576;   // 0..127
     const int g = h / a.hpg;
     const __nv_bfloat16 *px = static_cast<const __nv_bfloat16 *>(a.in[0]) + (size_t)h * kP;
     const __nv_bfloat16 *pB = static_cast<const __nv_bfloat16 *>(a.in[1]) + (size_t)g * N;
@@ -366,7 +382,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  if (warp == 12) {
+  if (warp == 16) {
     if (*abort) {   // products may still be in flight: wait for them before their memory goes
       if (lane == 0) {
         umma::commit(bar + kDrain);
