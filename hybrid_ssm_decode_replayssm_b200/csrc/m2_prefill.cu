@@ -9,7 +9,9 @@
 //   CB    = C B^T            [t, s]  both operands bf16 inputs: exact products
 //   inter = C h^T            [t, p]  h in three bf16 parts
 //   upd   = B^T (fw x)       [n, p]  fw x in three parts: the state's update, transposed
-//   intra = L x              [t, p]  L in three parts, in tensor memory as the A operand
+//   intra = L x              [t, p]  L in three parts; adds to e^{G_t} inter
+// (C and L are operands in tensor memory: reading all of them from shared memory costs
+// more than the tensor core's own time)
 // (a three-part split carries fp32 to 2^-24, so outputs and states keep fp32
 // accuracy).  The state lives in registers, one column n per thread; it is never
 // scaled in tensor memory.  G is a double prefix sum kept as two floats, so
@@ -44,13 +46,14 @@ constexpr int kOffH = 8 * kBlk;        // three parts of the state, [n][p]
 constexpr int kOffXp = 11 * kBlk;      // three parts of fw x, [s][p]
 constexpr int kYRow = 272;             // bytes per token of the outputs on their way out
 constexpr int kOffSc = 14 * kBlk;      // float4 (G hi, G lo, dt, fw) per token
-constexpr int kOffBar = kOffSc + kT * 16;
-enum { kFull0 = 0, kFull1, kCb, kInter, kUpd, kIntra, kL0, kL1, kHp, kXp, kXfree, kYfree, kScFull, kScFree, kStage0, kStage1,
+constexpr int kOffOd = kOffSc + kT * 16;   // e^{G_32w - G_s} dt_s for the rows of block w = 1, 2, 3
+constexpr int kOffBar = kOffOd + 192 * 4;
+enum { kFull0 = 0, kFull1, kCt, kCb, kInter, kYs, kUpd, kIntra, kL0, kL1, kHp, kXp, kXfree, kYfree, kScFull, kScFree, kStage0, kStage1,
        kDrain, kBars };
 constexpr int kSmemM = kOffBar + kBars * 8 + 32;
 static_assert(kSmemM <= 232448, "shared memory of one CTA");
-// tensor memory columns
-constexpr int kTmCb = 0, kTmInter = 128, kTmIntra = 192, kTmU = 256, kTmL = 320;
+// tensor memory columns (kTmC: C as an operand)
+constexpr int kTmCb = 0, kTmY = 128, kTmC = 192, kTmU = 256, kTmL = 320;
 
 template <int N>
 __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArgs a) {
@@ -67,7 +70,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
   float4 *sc = reinterpret_cast<float4 *>(smem + kOffSc);
   const uint32_t base = smem_u32(smem);
   if (t == 0) {
-    const int count[kBars] = {128, 128, 1, 1, 1, 1, 8, 8, 8, 8, 8, 8, 1, 16, 8, 8, 1};
+    const int count[kBars] = {128, 128, 8, 1, 1, 8, 1, 1, 8, 8, 8, 8, 8, 8, 1, 16, 8, 8, 1};
     for (int i = 0; i < kBars; ++i) mbar_init(bar + i, count[i]);
     *abort = 0;
     mbar_fence_init();
@@ -109,15 +112,29 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       if (!warp_wait(bar + kScFull, ph, abort, lim) || !warp_wait(bar + kCb, ph, abort, lim)) break;
       umma::fence_after_sync();
       const float4 me = sc[row];
+      // below the diagonal blocks e^{G_t - G_s} splits at the block's start, and one
+      // factor per column is left
+      const float4 ref = sc[w > 0 ? w * 32 - 1 : 0];
+      const float at = ex2((me.x - ref.x) + (me.y - ref.y));
+      const float *od = reinterpret_cast<const float *>(smem + kOffOd) + (w == 3 ? 96 : w == 2 ? 32 : 0);
+      bool ok = true;
       for (int cb = 0; cb < 4; ++cb) {
         if (cb <= w) {
+          const int c0 = cb * 32 + wg * 16;
           float v[16];
-          umma::ld_32x32b_x16(lanes + kTmCb + cb * 32 + wg * 16, v);
+          umma::ld_32x32b_x16(lanes + kTmCb + c0, v);
+          if (cb < w) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float4 s = sc[cb * 32 + wg * 16 + j];
-            v[j] = ex2((me.x - s.x) + (me.y - s.y)) * (s.z * v[j]);
-            if (cb == w) v[j] = wg * 16 + j <= lane ? v[j] : 0.f;
+            for (int j = 0; j < 16; j += 4) {
+              const float4 f = *reinterpret_cast<const float4 *>(od + c0 + j);
+              v[j] *= at * f.x; v[j + 1] *= at * f.y; v[j + 2] *= at * f.z; v[j + 3] *= at * f.w;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float4 s = sc[c0 + j];
+              v[j] = wg * 16 + j <= lane ? ex2((me.x - s.x) + (me.y - s.y)) * (s.z * v[j]) : 0.f;
+            }
           }
           split_store(lanes + kTmL + cb * 16 + wg * 8, 64, v);
         }
@@ -126,33 +143,45 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
           umma::fence_before_sync();
           warp_arrive(bar + kL0 + (cb >> 1));
         }
+        if (cb == 1) {   // e^{G_t} C h^T, in its place; the masked product adds to it
+          ok = warp_wait(bar + kInter, ph, abort, lim);
+          if (!ok) break;
+          umma::fence_after_sync();
+          const float g = ex2(me.x + me.y);
+#pragma unroll
+          for (int c = 0; c < 32; c += 16) {
+            float v[16];
+            uint32_t o[16];
+            umma::ld_32x32b_x16(lanes + kTmY + wg * 32 + c, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(g * v[j]);
+            st_x16(lanes + kTmY + wg * 32 + c, o);
+          }
+          wait_st();
+          umma::fence_before_sync();
+          warp_arrive(bar + kYs);
+        }
       }
+      if (!ok) break;
       warp_arrive(bar + kScFree);
-      if (!warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim) || !warp_wait(bar + kInter, ph, abort, lim)) break;
+      if (!warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim) || !warp_wait(bar + kIntra, ph, abort, lim)) break;
       umma::fence_after_sync();
-      const float g = ex2(me.x + me.y);
       const uint8_t *xrow = smem + kOffX + (i & 1) * kBlk;
       float y[32];
-      umma::ld_32x32b_x32(lanes + kTmInter + wg * 32, y);
+      umma::ld_32x32b_x32(lanes + kTmY + wg * 32, y);
+      umma::fence_before_sync();
+      warp_arrive(bar + kYfree);
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
         const uint4 raw = *reinterpret_cast<const uint4 *>(xrow + sw128(row, wg * 4 + j / 8));
         const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          y[j + 2 * k] = fmaf(g, y[j + 2 * k], Dh * __uint_as_float(x[k] << 16));
-          y[j + 2 * k + 1] = fmaf(g, y[j + 2 * k + 1], Dh * __uint_as_float(x[k] & 0xFFFF0000u));
+          y[j + 2 * k] = fmaf(Dh, __uint_as_float(x[k] << 16), y[j + 2 * k]);
+          y[j + 2 * k + 1] = fmaf(Dh, __uint_as_float(x[k] & 0xFFFF0000u), y[j + 2 * k + 1]);
         }
       }
-      if (!warp_wait(bar + kIntra, ph, abort, lim)) break;
-      umma::fence_after_sync();
-      float v[32];
-      umma::ld_32x32b_x32(lanes + kTmIntra + wg * 32, v);
-      umma::fence_before_sync();
-      warp_arrive(bar + kYfree);
       warp_arrive(bar + kStage0 + (i & 1));
-#pragma unroll
-      for (int j = 0; j < 32; ++j) y[j] += v[j];
       // y leaves through the place of fw x (read by now), four rows per store: a token per
       // lane would touch 32 lines per store and hold up all of shared memory
       uint8_t *stage = smem + kOffXp + w * 32 * kYRow + wg * 128;
@@ -203,8 +232,19 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
     }
     for (int i = 0; i < chunks; ++i) {
       const uint32_t ph = i & 1;
-      good = warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim) && warp_wait(bar + kScFull, ph, abort, lim) &&
-             (i == 0 || warp_wait(bar + kXfree, ph ^ 1, abort, lim));
+      good = warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim);
+      if (!good) break;
+      {   // C to tensor memory, where two products take it from without reading shared memory
+        uint4 v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4 *>(smem + kOffC + wg * kBlk + sw128(n, c));
+        st_x16(lanes + kTmC + wg * 32, *reinterpret_cast<const uint32_t (*)[16]>(&v[0]));
+        st_x16(lanes + kTmC + wg * 32 + 16, *reinterpret_cast<const uint32_t (*)[16]>(&v[4]));
+        wait_st();
+        umma::fence_before_sync();
+        warp_arrive(bar + kCt);
+      }
+      good = warp_wait(bar + kScFull, ph, abort, lim) && (i == 0 || warp_wait(bar + kXfree, ph ^ 1, abort, lim));
       if (!good) break;
       const float dec = *s_last;
       const uint8_t *x = smem + kOffX + (i & 1) * kBlk;
@@ -250,15 +290,15 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
     // each addition, and only those of the last, large part then count
     for (int i = 0; i < chunks; ++i) {
       const uint32_t ph = i & 1;
-      const uint32_t Bt = base + kOffB + (i & 1) * 2 * kBlk, Ct = base + kOffC, Xt = base + kOffX + (i & 1) * kBlk;
+      const uint32_t Bt = base + kOffB + (i & 1) * 2 * kBlk, Xt = base + kOffX + (i & 1) * kBlk;
       auto kmaj = [](uint32_t tile, int k) { return desc_sw128(tile + (k / 4) * kBlk + (k % 4) * 32, 16); };
       auto mnmaj = [](uint32_t tile, int k) { return desc_sw128(tile + k * 2048, kBlk); };
-      if (!warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim)) break;
+      if (!warp_wait(bar + kFull0 + (i & 1), (i >> 1) & 1, abort, lim) || !warp_wait(bar + kCt, ph, abort, lim)) break;
       umma::fence_after_sync();
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < KN; ++k)
-          umma::mma_bf16(tm + kTmCb, kmaj(Ct, k), kmaj(Bt, k), idesc(128, 128, false, false), k > 0);
+          mma_ts(tm + kTmCb, tm + kTmC + k * 8, kmaj(Bt, k), idesc(128, 128, false, false), k > 0);
         umma::commit(bar + kCb);
       }
       __syncwarp();
@@ -270,8 +310,8 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
         for (int p = 2; p >= 0; --p)
 #pragma unroll
           for (int k = 0; k < KN; ++k)
-            umma::mma_bf16(tm + kTmInter, kmaj(Ct, k), mnmaj(base + kOffH + p * kBlk, k), idesc(128, kP, false, true),
-                           p < 2 || k > 0);
+            mma_ts(tm + kTmY, tm + kTmC + k * 8, mnmaj(base + kOffH + p * kBlk, k), idesc(128, kP, false, true),
+                   p < 2 || k > 0);
         umma::commit(bar + kInter);
       }
       __syncwarp();
@@ -290,7 +330,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       bool ok = true;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        ok = ok && warp_wait(bar + kL0 + half, ph, abort, lim);
+        ok = ok && warp_wait(bar + kL0 + half, ph, abort, lim) && (half > 0 || warp_wait(bar + kYs, ph, abort, lim));
         if (!ok) break;
         umma::fence_after_sync();
         if (elect_one()) {
@@ -298,8 +338,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
           for (int p = 2; p >= 0; --p)
 #pragma unroll
             for (int k = half * 4; k < half * 4 + 4; ++k)
-              mma_ts(tm + kTmIntra, tm + kTmL + p * 64 + k * 8, mnmaj(Xt, k), idesc(128, kP, false, true),
-                     half > 0 || p < 2 || k > 0);
+              mma_ts(tm + kTmY, tm + kTmL + p * 64 + k * 8, mnmaj(Xt, k), idesc(128, kP, false, true), true);
         }
         __syncwarp();
       }
@@ -336,12 +375,19 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
         if (lane >= o) inc += up;
       }
       const double before = inc - sum, last = __shfl_sync(0xffffffffu, inc, 31);
+      const double at[3] = {__shfl_sync(0xffffffffu, inc, 7), __shfl_sync(0xffffffffu, inc, 15),
+                            __shfl_sync(0xffffffffu, inc, 23)};   // G at the ends of 32, 64, 96 tokens
       if (i > 0 && !warp_wait(bar + kScFree, (i - 1) & 1, abort, lim)) break;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const double g = G[k] + before;
         const float hi = (float)g;
         sc[lane * 4 + k] = make_float4(hi, (float)(g - (double)hi), dt[k], dt[k] * ex2((float)(last - g)));
+        const int s = lane * 4 + k;
+        float *od = reinterpret_cast<float *>(smem + kOffOd);
+#pragma unroll
+        for (int w = 1; w < 4; ++w)
+          if (s < 32 * w) od[(w == 3 ? 96 : w == 2 ? 32 : 0) + s] = dt[k] * ex2((float)(at[w - 1] - g));
         dt[k] = next[k];
       }
       if (lane == 0) *s_last = ex2((float)last);
@@ -368,7 +414,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       if (i > 1 && !warp_wait(bar + kStage0 + st, ((i >> 1) - 1) & 1, abort, lim)) break;
       tile(base + kOffB + st * 2 * kBlk, pB, a.stride[1], i, N);
       tile(base + kOffX + st * kBlk, px, a.stride[0], i, kP);
-      if (i > 0 && !warp_wait(bar + kInter, (i - 1) & 1, abort, lim)) break;
+      if (i > 0 && !warp_wait(bar + kCt, (i - 1) & 1, abort, lim)) break;
       tile(base + kOffC, pC, a.stride[2], i, N);
       cp_commit();
       cp_wait<0>();
