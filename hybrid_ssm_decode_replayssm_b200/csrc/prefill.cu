@@ -2,7 +2,7 @@
 // rows' checkpoints (or zero) to their new checkpoints, with every output.
 //
 //   plan_prefill_kernel   decides each sequence from the pointers (one CTA)
-//   scan_kernel           token by token, the state in registers
+//   scan_kernel           four tokens at a time, the state in registers
 //   requantize_kernel     the read copies of the rows written
 #include "rssm_prefill.h"
 #include "slots.cuh"
@@ -86,161 +86,400 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
   }
 }
 
-// ----------------------------------------------------------- token by token
-// One CTA of 128 threads per (sequence, head, 32 state rows); a thread holds 16
-// columns of two rows.  All three recurrences read the state before the token,
-//   z = S (g q),  u = S (g k),  w = beta (v - u)   (Mamba-2: w = dt x, no u)
-//   out = z + w (k.q),  S <- S g + w k^T
-// with g the gate (a scalar, or one per channel for KDA) and k, q, w = B, C, dt x
-// for Mamba-2, so both reductions over a row go together and one token costs one
-// round of shuffles.  Bound by that chain of latencies, and with many sequences
-// by the CUDA cores (4 operations per state element and token).
-constexpr int kScanThreads = 128;
-constexpr int kScanRows = 32;
-constexpr int kScanTok = 16;   // tokens staged in shared memory at a time
+// -------------------------------------------------------- four tokens at a time
+// One CTA of 256 threads per (sequence, head, 64 state rows): four warps run the
+// recurrence, the state in registers (16 columns of four rows per thread, two at dstate
+// 64, as packed pairs); four warps bring the tokens, eight at a time, as fp32 into two buffers of
+// shared memory, with what depends on the tokens alone, and take the outputs away.
+// Four tokens i = 0..3 go together: with p_i the product of their gates up to i and
+// d_ij that of the gates j+1..i (products, never ratios),
+//   u_i = S k_i,  z_i = S q_i                              (S before the four)
+//   w_i = b_i v_i - b_i p_i u_i - sum_{j<i} b_i d_ij (k_i.k_j) w_j
+//   o_i = scale (p_i z_i + sum_{j<=i} d_ij (q_i.k_j) w_j)
+//   S  <- p_3 S + sum_j d_3j w_j k_j^T
+// so the sums of a row cross the lanes in two rounds instead of eight, and an element
+// costs 3.25 multiply-adds per token instead of 4.  Mamba-2: k, q, v = B, C, x,
+// no u, w = dt x.  KDA: one gate per channel, so p and d go into the vectors (p_i k_i,
+// p_i q_i, d_3j k_j).  Bound by the CUDA cores' issue and the round's latency.
+constexpr int kScanThreads = 256;
+constexpr int kScanRows = 64;
+constexpr int kScanTok = 8;    // tokens per buffer: two blocks of four
+constexpr int kScanOcc = 4;    // CTAs per SM of the grid at most
+
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float x, float y) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float sum2(f32x2 v) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+  return x + y;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 template <typename T> __device__ __forceinline__ float ld_in(const void *p, int64_t i) {
   return to_f32<T>(__ldg(static_cast<const T *>(p) + i));
 }
+// Eight consecutive elements (16-byte aligned), as they come and as fp32.
+template <typename T> struct Raw8 {
+  uint4 x[sizeof(T) / 2];
+};
+template <typename T> __device__ __forceinline__ void ld8(Raw8<T> &o, const T *p) {
+#pragma unroll
+  for (int c = 0; c < (int)sizeof(T) / 2; ++c) o.x[c] = __ldg(reinterpret_cast<const uint4 *>(p) + c);
+}
+template <typename T> __device__ __forceinline__ void widen(float (&o)[8], const Raw8<T> &r) {
+  const T *e = reinterpret_cast<const T *>(r.x);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = to_f32<T>(e[j]);
+}
+__device__ __forceinline__ void named_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+// What the tokens of a block give: b (Mamba-2: dt), b p, scale p, d_3j, p_3, and by rows the
+// two triangles b_i d_ij (k_i.k_j) and scale d_ij (q_i.k_j).
+struct __align__(16) ScanBlock {
+  float be[4], bg[4], p[4], f[4];
+  float A[4][4], M[4][4];
+  float pc, pad[3];
+};
 
 template <int KIND, typename Tin, int C>
-__global__ void __launch_bounds__(kScanThreads) scan_kernel(const PrefillArgs a) {
+__global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const PrefillArgs a, int items) {
   constexpr bool M2 = KIND == RSSM_MAMBA2, KDA = KIND == RSSM_KDA;
   constexpr int LPR = C / 16;                       // lanes per row
-  constexpr int GROUPS = kScanThreads / LPR;        // row pairs per pass: 16 or 32
-  constexpr int RPT = kScanRows / GROUPS;           // rows per thread: 2 or 1
-  constexpr int kPer = 16 / sizeof(Tin);
+  constexpr int GROUPS = 128 / LPR;                 // rows per pass: 16 or 32
+  constexpr int RPT = kScanRows / GROUPS;           // rows per thread: 4 or 2
+  constexpr int NV = RPT * 4;                       // a thread's sums for four tokens
+  static_assert(NV == 2 * LPR, "of which it keeps two");
+  struct Buf {
+    float k[kScanTok][C], q[kScanTok][C];           // KDA: p_i k_i, p_i q_i
+    float kt[KDA ? kScanTok : 1][C], pc[KDA ? 2 : 1][C];   // KDA: d_3j k_j, p_3
+    float v[kScanTok][kScanRows], o[kScanTok][kScanRows];
+    ScanBlock blk[2];
+  };
+  __shared__ __align__(16) Buf buf[2];
+  __shared__ __align__(16) float raw_k[KDA ? kScanTok : 1][C], raw_g[KDA ? kScanTok : 1][C];
+  __shared__ __align__(16) float s_gate[kScanTok], s_beta[kScanTok];
   const int slices = a.R / kScanRows;
-  const int h = (int)(blockIdx.x % a.H), sl = (int)(blockIdx.x / a.H % slices);
-  const PrefillSeq q = a.seqs[blockIdx.x / a.H / slices];
-  if (q.dst < 0) return;
-  __shared__ __align__(16) float s_k[kScanTok][C], s_q[kScanTok][C];
-  __shared__ __align__(16) float s_g[KDA ? kScanTok : 1][C];
-  __shared__ float s_v[kScanTok][kScanRows], s_o[kScanTok][kScanRows];
-  __shared__ float s_a[kScanTok], s_b[kScanTok], s_kq[kScanTok];
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int sub = t % LPR, grp = t / LPR;
+  const int t = threadIdx.x, lane = t & 31;
   const size_t tile = (size_t)a.R * C;
-  float S[RPT][16];
-#pragma unroll
-  for (int r = 0; r < RPT; ++r) {
-    const int row = sl * kScanRows + grp + r * GROUPS;
-    const float *src = a.hc + ((size_t)q.src * a.H + h) * tile + (size_t)row * C;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float4 v = q.src < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : ld_stream(src + c * (C / 4) + sub * 4);
-      S[r][4 * c] = v.x; S[r][4 * c + 1] = v.y; S[r][4 * c + 2] = v.z; S[r][4 * c + 3] = v.w;
-    }
-  }
-  const float Ah = M2 ? __ldg(a.A + h) : 0.f, Dh = M2 ? __ldg(a.D + h) : 0.f;
-  const int hk = M2 ? h / a.hpg : h;                 // head (or group) of k and q
-  const Tin *pk = static_cast<const Tin *>(a.in[1]) + (size_t)hk * C;
-  const Tin *pq = static_cast<const Tin *>(a.in[M2 ? 2 : 0]) + (size_t)hk * C;
-  const Tin *pv = static_cast<const Tin *>(a.in[M2 ? 0 : 2]) + (size_t)h * a.R + sl * kScanRows;
-  const int64_t dk = a.stride[1], dq = a.stride[M2 ? 2 : 0], dv = a.stride[M2 ? 0 : 2];
-  for (int t0 = 0; t0 < q.n; t0 += kScanTok) {
-    const int m = min(kScanTok, q.n - t0);
-    const int64_t tok = q.tok + t0;
-    __syncthreads();
-    for (int i = t; i < m * (C / kPer); i += kScanThreads) {
-      const int e = i / (C / kPer), c = i % (C / kPer) * kPer;
-      stage_row<Tin>(&s_k[e][c], pk + (tok + e) * dk + c, kPer, 0, 1);
-      stage_row<Tin>(&s_q[e][c], pq + (tok + e) * dq + c, kPer, 0, 1);
-    }
-    for (int i = t; i < m * (kScanRows / kPer); i += kScanThreads) {
-      const int e = i / (kScanRows / kPer), c = i % (kScanRows / kPer) * kPer;
-      stage_row<Tin>(&s_v[e][c], pv + (tok + e) * dv + c, kPer, 0, 1);
-    }
-    if constexpr (KDA)
-      for (int i = t; i < m * (C / 4); i += kScanThreads) {
-        const int e = i / (C / 4), c = i % (C / 4) * 4;
-        *reinterpret_cast<float4 *>(&s_g[e][c]) = __ldg(reinterpret_cast<const float4 *>(
-            static_cast<const float *>(a.in[3]) + (tok + e) * a.stride[3] + (size_t)h * C + c));
-      }
-    if (t < m) {
-      if constexpr (M2) {
-        const float dt = ld_in<Tin>(a.in[3], (tok + t) * a.stride[3] + h);
-        s_a[t] = expf(dt * Ah);
-        s_b[t] = dt;
-      } else {
-        if constexpr (!KDA) s_a[t] = ld_in<float>(a.in[3], (tok + t) * a.stride[3] + h);
-        s_b[t] = ld_in<float>(a.in[4], (tok + t) * a.stride[4] + h);
-      }
-    }
-    __syncthreads();
-    for (int e = warp; e < m; e += kScanThreads / 32) {
-      float d = 0.f;
-#pragma unroll
-      for (int c = 0; c < C; c += 32) d = fmaf(s_k[e][c + lane], s_q[e][c + lane], d);
-      d = warp_sum(d);
-      if (lane == 0) s_kq[e] = d;
-    }
-    __syncthreads();
-    for (int e = 0; e < m; ++e) {
-      float k[16], qv[16];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        *reinterpret_cast<float4 *>(k + 4 * c) = *reinterpret_cast<const float4 *>(&s_k[e][c * (C / 4) + sub * 4]);
-        *reinterpret_cast<float4 *>(qv + 4 * c) = *reinterpret_cast<const float4 *>(&s_q[e][c * (C / 4) + sub * 4]);
-      }
-      const float al = KDA ? 1.f : s_a[e], be = s_b[e], kq = s_kq[e];
-      float u[RPT], z[RPT];
-      if constexpr (KDA) {   // decay the state first: one product per element serves both dots
-        float g[16];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<float4 *>(g + 4 * c) = *reinterpret_cast<const float4 *>(&s_g[e][c * (C / 4) + sub * 4]);
-#pragma unroll
-        for (int r = 0; r < RPT; ++r)
-#pragma unroll
-          for (int c = 0; c < 16; ++c) S[r][c] *= g[c];
-      }
+  // barriers: 1, 2 a buffer is full; 3, 4 it is empty; 5 the bringing warps among themselves
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int h = item % a.H, sl = item / a.H % slices;
+    const PrefillSeq q = a.seqs[item / a.H / slices];
+    if (q.dst < 0 || q.n > a.scan_most) continue;
+    const int tiles = (q.n + kScanTok - 1) / kScanTok;
+    if (t < 128) {
+      // ------------------------------------------------ the recurrence
+      const int sub = t % LPR, grp = t / LPR, lane0 = lane - sub;
+      const int mine = grp + sub / 2 * GROUPS, i0 = sub % 2 * 2;   // the row and tokens whose sums this lane keeps
+      f32x2 S[RPT][8];
 #pragma unroll
       for (int r = 0; r < RPT; ++r) {
-        float u0 = 0.f, u1 = 0.f, z0 = 0.f, z1 = 0.f;
+        const int row = sl * kScanRows + grp + r * GROUPS;
+        const float *src = a.hc + ((size_t)(q.src < 0 ? 0 : q.src) * a.H + h) * tile + (size_t)row * C;
 #pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-          z0 = fmaf(S[r][c], qv[c], z0);
-          z1 = fmaf(S[r][c + 1], qv[c + 1], z1);
+        for (int c = 0; c < 4; ++c) {
+          const float4 v = q.src < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : ld_stream(src + c * (C / 4) + sub * 4);
+          S[r][2 * c] = pack2(v.x, v.y);
+          S[r][2 * c + 1] = pack2(v.z, v.w);
+        }
+      }
+      const float Dh = M2 ? __ldg(a.D + h) : 0.f;
+      for (int n = 0; n < tiles; ++n) {
+        Buf &B = buf[n & 1];
+        const int blocks = q.n - n * kScanTok > 4 ? 2 : 1;
+        named_sync(1 + (n & 1), kScanThreads);
+#pragma unroll 1
+        for (int b = 0; b < blocks; ++b) {
+          const ScanBlock &K = B.blk[b];
+          const float4 be = *reinterpret_cast<const float4 *>(K.be);
+          float w[4] = {be.x * B.v[b * 4][mine], be.y * B.v[b * 4 + 1][mine], be.z * B.v[b * 4 + 2][mine],
+                        be.w * B.v[b * 4 + 3][mine]};
+          // sums[0], sums[1]: S x_i of row mine and tokens i0, i0 + 1 (whole, over the lanes)
+          float u[M2 ? 2 : NV], z[NV];
+          {
+            f32x2 au[M2 ? 1 : NV], az[NV];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+              az[j] = 0;
+              if constexpr (!M2) au[j] = 0;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if constexpr (!M2) {
+                  const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&B.k[b * 4 + i][c * (C / 4) + sub * 4]);
+#pragma unroll
+                  for (int r = 0; r < RPT; ++r)
+                    au[r * 4 + i] = fma2(S[r][2 * c + 1], x.y, fma2(S[r][2 * c], x.x, au[r * 4 + i]));
+                }
+                const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(&B.q[b * 4 + i][c * (C / 4) + sub * 4]);
+#pragma unroll
+                for (int r = 0; r < RPT; ++r)
+                  az[r * 4 + i] = fma2(S[r][2 * c + 1], y.y, fma2(S[r][2 * c], y.x, az[r * 4 + i]));
+              }
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+              z[j] = sum2(az[j]);
+              if constexpr (!M2) u[j] = sum2(au[j]);
+            }
+          }
+          if constexpr (!M2) tr_sum<NV, LPR / 2>(u, lane);
+          tr_sum<NV, LPR / 2>(z, lane);
           if constexpr (!M2) {
-            u0 = fmaf(S[r][c], k[c], u0);
-            u1 = fmaf(S[r][c + 1], k[c + 1], u1);
+            const float x0 = __shfl_xor_sync(kFull, u[0], 1), x1 = __shfl_xor_sync(kFull, u[1], 1);
+            const float u4[4] = {i0 ? x0 : u[0], i0 ? x1 : u[1], i0 ? u[0] : x0, i0 ? u[1] : x1};
+            const float4 bg = *reinterpret_cast<const float4 *>(K.bg);
+            const float4 a1 = *reinterpret_cast<const float4 *>(K.A[1]), a2 = *reinterpret_cast<const float4 *>(K.A[2]);
+            const float4 a3 = *reinterpret_cast<const float4 *>(K.A[3]);
+            w[0] = fmaf(-bg.x, u4[0], w[0]);
+            w[1] = fmaf(-a1.x, w[0], fmaf(-bg.y, u4[1], w[1]));
+            w[2] = fmaf(-a2.y, w[1], fmaf(-a2.x, w[0], fmaf(-bg.z, u4[2], w[2])));
+            w[3] = fmaf(-a3.z, w[2], fmaf(-a3.y, w[1], fmaf(-a3.x, w[0], fmaf(-bg.w, u4[3], w[3]))));
+          }
+          const float4 f4 = *reinterpret_cast<const float4 *>(K.f);
+          const float fs[4] = {f4.x, f4.y, f4.z, f4.w};
+          f32x2 fw[RPT][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float own = KDA ? w[j] : fs[j] * w[j];
+#pragma unroll
+            for (int r = 0; r < RPT; ++r) {
+              const float x = __shfl_sync(kFull, own, lane0 + 2 * r);
+              fw[r][j] = pack2(x, x);
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {   // the outputs of this lane's row and tokens
+            const int i = i0 + s;
+            const float4 m = *reinterpret_cast<const float4 *>(K.M[i]);
+            const float o = fmaf(m.x, w[0], fmaf(m.y, w[1], fmaf(m.z, w[2], fmaf(m.w, w[3], K.p[i] * z[s]))));
+            B.o[b * 4 + i][mine] = M2 ? fmaf(Dh, B.v[b * 4 + i][mine], o) : o;
+          }
+          asm volatile("" ::: "memory");   // k is read again: there are no registers to keep it
+          const f32x2 pc = pack2(K.pc, K.pc);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            ulonglong2 g = make_ulonglong2(pc, pc);
+            if constexpr (KDA) g = *reinterpret_cast<const ulonglong2 *>(&B.pc[b][c * (C / 4) + sub * 4]);
+#pragma unroll
+            for (int r = 0; r < RPT; ++r) {
+              S[r][2 * c] = mul2(S[r][2 * c], g.x);
+              S[r][2 * c + 1] = mul2(S[r][2 * c + 1], g.y);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float *kv = KDA ? &B.kt[b * 4 + j][c * (C / 4) + sub * 4] : &B.k[b * 4 + j][c * (C / 4) + sub * 4];
+              const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(kv);
+#pragma unroll
+              for (int r = 0; r < RPT; ++r) {
+                S[r][2 * c] = fma2(fw[r][j], x.x, S[r][2 * c]);
+                S[r][2 * c + 1] = fma2(fw[r][j], x.y, S[r][2 * c + 1]);
+              }
+            }
           }
         }
-        u[r] = u0 + u1;
-        z[r] = z0 + z1;
+        named_arrive(3 + (n & 1), kScanThreads);
       }
-#pragma unroll
-      for (int o = LPR / 2; o >= 1; o >>= 1)
-#pragma unroll
-        for (int r = 0; r < RPT; ++r) {
-          z[r] += __shfl_xor_sync(kFull, z[r], o);
-          if constexpr (!M2) u[r] += __shfl_xor_sync(kFull, u[r], o);
-        }
 #pragma unroll
       for (int r = 0; r < RPT; ++r) {
-        const float v = s_v[e][grp + r * GROUPS];
-        const float w = M2 ? be * v : be * fmaf(-al, u[r], v);
-        const float o = fmaf(al, z[r], w * kq);
-        if (sub == 0) s_o[e][grp + r * GROUPS] = M2 ? fmaf(Dh, v, o) : a.out_scale * o;
+        const int row = sl * kScanRows + grp + r * GROUPS;
+        float *dst = a.hc + ((size_t)q.dst * a.H + h) * tile + (size_t)row * C;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) S[r][c] = KDA ? fmaf(w, k[c], S[r][c]) : fmaf(al, S[r][c], w * k[c]);
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<ulonglong2 *>(dst + c * (C / 4) + sub * 4) = make_ulonglong2(S[r][2 * c], S[r][2 * c + 1]);
+      }
+    } else {
+      // ------------------------------------------------ tokens in, outputs out
+      const int l = t - 128;
+      const int hk = M2 ? h / a.hpg : h;                 // head (or group) of k and q
+      const Tin *pk = static_cast<const Tin *>(a.in[1]) + (size_t)hk * C;
+      const Tin *pq = static_cast<const Tin *>(a.in[M2 ? 2 : 0]) + (size_t)hk * C;
+      const Tin *pv = static_cast<const Tin *>(a.in[M2 ? 0 : 2]) + (size_t)h * a.R + sl * kScanRows;
+      const int64_t dk = a.stride[1], dq = a.stride[M2 ? 2 : 0], dv = a.stride[M2 ? 0 : 2];
+      const float Ah = M2 ? __ldg(a.A + h) : 0.f;
+      const float scale = M2 ? 1.f : a.out_scale;
+      constexpr int per = C / 8;                         // threads per token: 16 or 8
+      const int e = l / per, c8 = l % per * 8;           // this thread's token and columns
+      const int bi = e & 3, bb = e & ~3;                 // its place in its block, and the block's first
+      const int ve = l / 16, vc = l % 16 * 4;            // and its four values of v
+      float k8[8], q8[8], g8[8];
+      // the next tile's values as they come: widened only when they are used, so that
+      // nothing waits for them before
+      Raw8<Tin> rk, rq;
+      Raw8<float> rg;
+      uint4 rv = make_uint4(0, 0, 0, 0);
+      Tin rdt = Tin(0.f);
+      float ra = 1.f, rb = 0.f;
+      auto load = [&](int n) {   // zeros behind the end: k = q = v = b = 0, gate 1
+        const int64_t tok = (int64_t)q.tok + n * kScanTok;
+        const int m = q.n - n * kScanTok;
+        if (m < kScanTok) {
+          const uint4 zero = make_uint4(0, 0, 0, 0), one = make_uint4(0x3F800000u, 0x3F800000u, 0x3F800000u, 0x3F800000u);
+#pragma unroll
+          for (int c = 0; c < (int)sizeof(Tin) / 2; ++c) rk.x[c] = rq.x[c] = zero;
+          rg.x[0] = rg.x[1] = one;
+          rv = zero;
+          rdt = Tin(0.f);
+          ra = 1.f;
+          rb = 0.f;
+        }
+        if (e < m && e < kScanTok) {
+          ld8<Tin>(rk, pk + (tok + e) * dk + c8);
+          ld8<Tin>(rq, pq + (tok + e) * dq + c8);
+          if constexpr (KDA)
+            ld8<float>(rg, static_cast<const float *>(a.in[3]) + (tok + e) * a.stride[3] + (size_t)h * C + c8);
+          if (c8 == 0) {
+            if constexpr (M2) {
+              rdt = __ldg(static_cast<const Tin *>(a.in[3]) + (tok + e) * a.stride[3] + h);
+            } else {
+              if constexpr (!KDA) ra = __ldg(static_cast<const float *>(a.in[3]) + (tok + e) * a.stride[3] + h);
+              rb = __ldg(static_cast<const float *>(a.in[4]) + (tok + e) * a.stride[4] + h);
+            }
+          }
+        }
+        if (ve < m) {
+          const Tin *p = pv + (tok + ve) * dv + vc;
+          if constexpr (sizeof(Tin) == 4) {
+            rv = __ldg(reinterpret_cast<const uint4 *>(p));
+          } else {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+            rv.x = x.x;
+            rv.y = x.y;
+          }
+        }
+      };
+      auto put8 = [&](float *p, const float *x) {
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+      };
+      auto flush = [&](int n) {   // the outputs of tile n
+        const int64_t tok = (int64_t)q.tok + n * kScanTok;
+        if (ve < q.n - n * kScanTok)
+          st_stream(a.out + ((tok + ve) * a.H + h) * a.R + sl * kScanRows + vc,
+                    *reinterpret_cast<const float4 *>(&buf[n & 1].o[ve][vc]));
+      };
+      if (tiles > 0) load(0);
+      for (int n = 0; n < tiles; ++n) {
+        Buf &B = buf[n & 1];
+        if (n > 1) {
+          named_sync(3 + (n & 1), kScanThreads);
+          flush(n - 2);
+        }
+        if (n > 0) named_sync(5, 128);   // the last tile's gates and keys are read
+        if (e < kScanTok) {
+          widen<Tin>(k8, rk);
+          widen<Tin>(q8, rq);
+          if constexpr (KDA) {
+            widen<float>(g8, rg);
+            put8(&raw_k[e][c8], k8);
+            put8(&raw_g[e][c8], g8);
+          } else {
+            put8(&B.k[e][c8], k8);
+            put8(&B.q[e][c8], q8);
+          }
+          if (c8 == 0) {
+            if constexpr (M2) {
+              const float dt = to_f32<Tin>(rdt);
+              s_gate[e] = expf(dt * Ah);
+              s_beta[e] = dt;
+            } else {
+              s_gate[e] = ra;
+              s_beta[e] = rb;
+            }
+          }
+        }
+        {
+          float4 x;
+          if constexpr (sizeof(Tin) == 4)
+            x = *reinterpret_cast<const float4 *>(&rv);
+          else
+            x = make_float4(__uint_as_float(rv.x << 16), __uint_as_float(rv.x & 0xFFFF0000u), __uint_as_float(rv.y << 16),
+                            __uint_as_float(rv.y & 0xFFFF0000u));
+          *reinterpret_cast<float4 *>(&B.v[ve][vc]) = x;
+        }
+        if (n + 1 < tiles) load(n + 1);
+        named_sync(5, 128);
+        if (e < kScanTok) {
+          float pair[8];   // k_i.k_j and q_i.k_j, j = 0..3, over this thread's columns
+          float D[8];      // KDA: d_ij of this thread's channels
+#pragma unroll
+          for (int j = 0; j < 8; ++j) pair[j] = 0.f, D[j] = 1.f;
+#pragma unroll
+          for (int j = 3; j >= 0; --j)
+            if (j <= bi) {
+              float x[8];
+              const float *kj = KDA ? &raw_k[bb + j][c8] : &B.k[bb + j][c8];
+              *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(kj);
+              *reinterpret_cast<float4 *>(x + 4) = *reinterpret_cast<const float4 *>(kj + 4);
+              if constexpr (KDA) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) x[c] *= D[c];
+                if (bi == 3) put8(&B.kt[bb + j][c8], x);
+              }
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                pair[j] = fmaf(k8[c], x[c], pair[j]);
+                pair[4 + j] = fmaf(q8[c], x[c], pair[4 + j]);
+              }
+              if constexpr (KDA) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) D[c] *= raw_g[bb + j][c8 + c];
+              }
+            }
+          if constexpr (KDA) {   // D is p_i now
+            if (bi == 3) put8(&B.pc[bb >> 2][c8], D);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) k8[c] *= D[c], q8[c] *= D[c];
+            put8(&B.k[e][c8], k8);
+            put8(&B.q[e][c8], q8);
+          }
+          tr_sum<8, per / 2>(pair, lane);
+          const int val = tr_base<8, per / 2>(lane), j = val & 3;
+          ScanBlock &K = B.blk[bb >> 2];
+          float d = 1.f, p = 1.f, f = 1.f;   // d_ij, p_i and d_3i of scalar gates
+          if constexpr (!KDA) {
+            const float4 g4 = *reinterpret_cast<const float4 *>(&s_gate[bb]);
+            const float g[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              if (r <= bi) p *= g[r];
+              if (r > j && r <= bi) d *= g[r];
+              if (r > bi) f *= g[r];
+            }
+          }
+          const float be = s_beta[e];
+          if (val < 4) K.A[bi][j] = j < bi ? be * d * pair[0] : 0.f;
+          else K.M[bi][j] = j <= bi ? scale * d * pair[0] : 0.f;
+          if (c8 == 0) {
+            K.be[bi] = be;
+            K.bg[bi] = be * p;
+            K.p[bi] = scale * p;
+            if (bi == 3) K.pc = p;
+            K.f[bi] = f;
+          }
+        }
+        named_arrive(1 + (n & 1), kScanThreads);
+      }
+      for (int n = max(0, tiles - 2); n < tiles; ++n) {
+        named_sync(3 + (n & 1), kScanThreads);
+        flush(n);
       }
     }
-    __syncthreads();
-    for (int i = t; i < m * (kScanRows / 4); i += kScanThreads) {
-      const int e = i / (kScanRows / 4), c = i % (kScanRows / 4) * 4;
-      st_stream(a.out + ((tok + e) * a.H + h) * a.R + sl * kScanRows + c, *reinterpret_cast<const float4 *>(&s_o[e][c]));
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < RPT; ++r) {
-    const int row = sl * kScanRows + grp + r * GROUPS;
-    float *dst = a.hc + ((size_t)q.dst * a.H + h) * tile + (size_t)row * C;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<float4 *>(dst + c * (C / 4) + sub * 4) =
-          make_float4(S[r][4 * c], S[r][4 * c + 1], S[r][4 * c + 2], S[r][4 * c + 3]);
+    __syncthreads();   // the buffers and barriers start anew
   }
 }
 
@@ -263,14 +502,17 @@ __global__ void __launch_bounds__(256) requantize_kernel(const PrefillArgs a) {
 
 template <int KIND, typename Tin>
 void launch_scan(const PrefillArgs &a, cudaStream_t s) {
-  const dim3 grid((unsigned)((size_t)a.n_seq * a.H * (a.R / kScanRows)));
+  const int items = (int)((size_t)a.n_seq * a.H * (a.R / kScanRows));
+  const dim3 grid((unsigned)(items < 148 * kScanOcc ? items : 148 * kScanOcc));
   if constexpr (KIND == RSSM_MAMBA2)
     if (a.C == 64) {
-      scan_kernel<KIND, Tin, 64><<<grid, kScanThreads, 0, s>>>(a);
+      scan_kernel<KIND, Tin, 64><<<grid, kScanThreads, 0, s>>>(a, items);
       return;
     }
-  scan_kernel<KIND, Tin, 128><<<grid, kScanThreads, 0, s>>>(a);
+  scan_kernel<KIND, Tin, 128><<<grid, kScanThreads, 0, s>>>(a, items);
 }
+
+constexpr int kScanMean = 0;
 
 size_t seq_bytes(int n_seq) { return ((size_t)n_seq * sizeof(PrefillSeq) + 255) & ~(size_t)255; }
 
@@ -288,10 +530,12 @@ cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *
   cudaError_t e = cudaGetLastError();
   ++*launches;
   if (e != cudaSuccess) return e;
+  a.scan_most = a.n_tokens;
   const bool bf16 = in_dtype == RSSM_BF16;
-  if (m2_chunk_path(a, in_dtype))
+  const bool few = a.n_tokens <= (long long)kScanMean * a.n_seq;
+  if (!few && m2_chunk_path(a, in_dtype))
     e = m2_chunk_prefill(a, s);
-  else if (gdn_chunk_path(a, in_dtype))
+  else if (!few && gdn_chunk_path(a, in_dtype))
     e = gdn_chunk_prefill(a, s);
   else switch (a.kind) {
     case RSSM_MAMBA2:

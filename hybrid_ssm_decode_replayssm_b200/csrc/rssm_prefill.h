@@ -17,6 +17,7 @@ struct PrefillArgs {
   int kind;
   int B, H, G, hpg, R, C;
   int n_seq, n_tokens;
+  int scan_most;              // longest sequence of the token-by-token kernel
   float out_scale;
   const float *A, *D;
   float *hc;

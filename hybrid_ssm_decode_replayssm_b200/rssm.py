@@ -12,6 +12,7 @@ handle, and exposes the calls with the same names minus the ``rssm_`` prefix.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -123,6 +124,16 @@ def check(code: int):
 
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
+
+
+@contextlib.contextmanager
+def _use(device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
 
 
 def _stream(stream) -> int:
@@ -243,25 +254,39 @@ class ReplayLayer:
         check(lib().rssm_branch(self.handle, parent.data_ptr(), _stream(stream)))
 
     def _row_list(self, t, n, name):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.shape != (n,) or \
-                not t.is_contiguous() or t.device != self.ckpt.device:
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or \
+                (n > 1 and t.stride(0) != 1) or t.device != self.ckpt.device:
             raise ValueError(f"{name} must be a contiguous int32 tensor of shape [{n}] on {self.ckpt.device}")
-        return t
 
-    def _token_shapes(self, T):
-        d = self.desc
-        H, R, Cc = d.nheads, d.headdim, d.dstate
-        t = torch.bfloat16 if d.in_dtype == RSSM_BF16 else torch.float32
-        if d.kind == RSSM_MAMBA2:
-            return [((T, H, R), t), ((T, d.ngroups, Cc), t), ((T, d.ngroups, Cc), t), ((T, H), t)]
-        gate = (T, H, Cc) if d.kind == RSSM_KDA else (T, H)
-        return [((T, H, Cc), t), ((T, H, Cc), t), ((T, H, R), t), (gate, torch.float32), ((T, H), torch.float32)]
+    def _token_inputs(self):
+        """Per prefill input: the shape and strides of one token, its dtype, and its elements."""
+        got = getattr(self, "_tokens", None)
+        if got is None:
+            d = self.desc
+            H, R, Cc = d.nheads, d.headdim, d.dstate
+            t, f = torch.bfloat16 if d.in_dtype == RSSM_BF16 else torch.float32, torch.float32
+            if d.kind == RSSM_MAMBA2:
+                each = [((H, R), t), ((d.ngroups, Cc), t), ((d.ngroups, Cc), t), ((H,), t)]
+            else:
+                each = [((H, Cc), t), ((H, Cc), t), ((H, R), t), ((H, Cc) if d.kind == RSSM_KDA else (H,), f), ((H,), f)]
+            got = [(s, (s[-1], 1) if len(s) == 2 else (1,), dt, s[0] * s[-1] if len(s) == 2 else s[0])
+                   for s, dt in each]
+            self._tokens, self._work_bytes = got, {}
+        return got
+
+    def _on_device(self, stream):
+        """The stream of a call, and a context that makes the layer's device and that stream current
+        (nothing where they are already)."""
+        dev = self.ckpt.device
+        if stream is None and torch.cuda.current_device() == dev.index:
+            return torch.cuda.current_stream(), contextlib.nullcontext()
+        return (torch.cuda.current_stream(dev) if stream is None else stream), _use(dev, stream)
 
     def prefill(self, inputs, offsets, out, rows=None, fresh=None, stream=None):
         """Run prompts through the layer: tokens offsets[i] .. offsets[i + 1] - 1 of the packed
         inputs ([tokens, H, ...], any stride between tokens) continue row rows[i], or start it
         anew where fresh[i] is nonzero.  ``out`` [tokens, H, headdim] fp32 gets the outputs."""
-        dev = self.ckpt.device
+        dev, d = self.ckpt.device, self.desc
         if not isinstance(out, torch.Tensor) or out.dim() != 3:
             raise ValueError("out must be a [tokens, heads, headdim] tensor")
         T, n = out.shape[0], offsets.numel() - 1
@@ -269,31 +294,35 @@ class ReplayLayer:
         for t, name in ((rows, "rows"), (fresh, "fresh")):
             if t is not None:
                 self._row_list(t, n, name)
-        shapes = self._token_shapes(T)
-        if len(inputs) != len(shapes):
-            raise ValueError(f"the layer takes {len(shapes)} inputs, got {len(inputs)}")
-        strides = (C.c_int64 * 5)()
-        for i, (t, (shape, dtype)) in enumerate(zip(inputs, shapes)):
-            if tuple(t.shape) != shape or t.dtype != dtype or t.device != dev:
-                raise ValueError(f"inputs[{i}] must be {dtype} {list(shape)} on {dev}, "
+        each = self._token_inputs()
+        if len(inputs) != len(each):
+            raise ValueError(f"the layer takes {len(each)} inputs, got {len(inputs)}")
+        ptrs, strides = (C.c_void_p * 5)(), (C.c_int64 * 5)()
+        for i, (t, (shape, inner, dtype, width)) in enumerate(zip(inputs, each)):
+            if t.dtype != dtype or t.device != dev or t.shape != (T,) + shape:
+                raise ValueError(f"inputs[{i}] must be {dtype} {[T, *shape]} on {dev}, "
                                  f"got {t.dtype} {list(t.shape)} on {t.device}")
-            width = t[0].numel() if T else 0
-            if T and not t[0].is_contiguous():
+            st = t.stride()
+            if T and st[1:] != inner and not t[0].is_contiguous():
                 raise ValueError(f"inputs[{i}]: the values of one token must be contiguous")
-            strides[i] = t.stride(0) if T > 1 else width
-        if tuple(out.shape) != (T, self.desc.nheads, self.desc.headdim) or out.dtype != torch.float32 or \
-                out.device != dev or not out.is_contiguous():
-            raise ValueError(f"out must be a contiguous fp32 [{T}, {self.desc.nheads}, {self.desc.headdim}] "
-                             f"tensor on {dev}")
-        nbytes = C.c_size_t()
-        check(lib().rssm_prefill_workspace_size(self.handle, n, T, C.byref(nbytes)))
-        with torch.cuda.device(dev):
-            s = torch.cuda.current_stream() if stream is None else stream
-            with torch.cuda.stream(s):   # the workspace belongs to the stream that uses it
-                work = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
-            check(lib().rssm_prefill(self.handle, n, T, offsets.data_ptr(), _ptr(rows), _ptr(fresh),
-                                     _ptr_array(inputs), strides if T else None, out.data_ptr(),
-                                     work.data_ptr(), nbytes.value, s.cuda_stream))
+            strides[i] = st[0] if T > 1 else width
+            ptrs[i] = t.data_ptr()
+        if out.shape != (T, d.nheads, d.headdim) or out.dtype != torch.float32 or out.device != dev or \
+                not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous fp32 [{T}, {d.nheads}, {d.headdim}] tensor on {dev}")
+        L = lib()
+        nbytes = self._work_bytes.get((n, T))
+        if nbytes is None:
+            size = C.c_size_t()
+            check(L.rssm_prefill_workspace_size(self.handle, n, T, C.byref(size)))
+            if len(self._work_bytes) > 4096:
+                self._work_bytes.clear()
+            nbytes = self._work_bytes[n, T] = size.value
+        s, ctx = self._on_device(stream)
+        with ctx:   # the workspace belongs to the stream that uses it
+            work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            check(L.rssm_prefill(self.handle, n, T, offsets.data_ptr(), _ptr(rows), _ptr(fresh), ptrs,
+                                 strides if T else None, out.data_ptr(), work.data_ptr(), nbytes, s.cuda_stream))
         return out
 
     def copy_rows(self, src, dst_rows, src_rows, stream=None):
@@ -304,19 +333,19 @@ class ReplayLayer:
         self._row_list(src_rows, n, "src_rows")
         if src.ckpt.device != self.ckpt.device:
             raise ValueError("both layers must be on one device")
-        with torch.cuda.device(self.ckpt.device):
+        s, ctx = self._on_device(stream)
+        with ctx:
             check(lib().rssm_copy_rows(self.handle, src.handle, n, dst_rows.data_ptr(), src_rows.data_ptr(),
-                                       _stream(stream)))
+                                       s.cuda_stream))
 
     def compact_rows(self, live, stream=None):
         """Pack the rows with nonzero ``live`` (int32 [B]) in front; returns (new_row [B], n_live [1])."""
         B = self.desc.batch
         self._row_list(live, B, "live")
-        with torch.cuda.device(self.ckpt.device):
-            s = torch.cuda.current_stream() if stream is None else stream
-            with torch.cuda.stream(s):
-                told = torch.empty(B + 1, dtype=torch.int32, device=self.ckpt.device)
-            new_row, n_live = told[:B], told[B:]
+        s, ctx = self._on_device(stream)
+        with ctx:
+            new_row = torch.empty(B, dtype=torch.int32, device=self.ckpt.device)
+            n_live = torch.empty(1, dtype=torch.int32, device=self.ckpt.device)
             check(lib().rssm_compact_rows(self.handle, live.data_ptr(), new_row.data_ptr(), n_live.data_ptr(),
                                           s.cuda_stream))
         return new_row, n_live
