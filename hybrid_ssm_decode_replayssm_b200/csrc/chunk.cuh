@@ -4,6 +4,7 @@
 #pragma once
 
 #include "rssm_device.cuh"
+#include "rssm_prefill.h"
 #include "umma.cuh"
 
 namespace rssm {
@@ -138,6 +139,40 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
 // All lanes wait; false (for all) once the CTA gives up.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, long long limit) {
   return warp_all(mbar_wait_bounded(bar, parity, abort, limit));
+}
+
+// Programmatic launches: wait for the grids before (complete, their writes visible), and
+// let the next one begin.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// The next (sequence, head) of a persistent chunk kernel, longest sequences first: every
+// thread of the CTA calls, having finished the one before.  False: none is left, or a
+// wait gave up.
+template <int THREADS, int BARS>
+__device__ __forceinline__ bool next_item(const PrefillArgs &a, uint64_t *bar, const int (&count)[BARS], int *s_item,
+                                          volatile int *abort, PrefillSeq &q, int &h) {
+  for (;;) {
+    umma::fence_before_sync();
+    named_sync(0, THREADS);
+    umma::fence_after_sync();
+    if (*abort) return false;
+    if (threadIdx.x == 0) {
+      *s_item = atomicAdd(a.queue + kChunkQueue, 1);
+#pragma unroll
+      for (int i = 0; i < BARS; ++i) {
+        asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar + i)) : "memory");
+        mbar_init(bar + i, count[i]);
+      }
+      mbar_fence_init();
+    }
+    named_sync(0, THREADS);
+    const int item = *s_item;
+    if (item >= a.queue[kLongCount] * a.H) return false;
+    q = a.seqs[item / a.H];
+    h = item % a.H;
+    if (q.dst >= 0 && q.n > a.scan_most) return true;
+  }
 }
 
 }  // namespace chunk

@@ -103,18 +103,14 @@ __device__ __forceinline__ void block_product(float (&o)[4][NC], const float *L,
 
 __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  const PrefillSeq q = a.seqs[blockIdx.x / a.H];
-  if (q.dst < 0) return;
-  const int h = (int)(blockIdx.x % a.H);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int chunks = (q.n + kT - 1) / kT;
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kOffBar);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + kOffBar + kBars * 8);
   uint32_t *tm_slot = reinterpret_cast<uint32_t *>(smem + kOffBar + kBars * 8 + 8);
   Scalars *scs = reinterpret_cast<Scalars *>(smem + kOffSc);
   const uint32_t base = smem_u32(smem);
+  constexpr int count[kBars] = {64, 64, 1, 1, 1, 1, 12, 12, 1, 1, 4, 4, 1, 1, 8, 8, 1, 1, 8, 1, 8, 8, 1, 4, 4, 1};
   if (t == 0) {
-    const int count[kBars] = {64, 64, 1, 1, 1, 1, 12, 12, 1, 1, 4, 4, 1, 1, 8, 8, 1, 1, 8, 1, 8, 8, 1, 4, 4, 1};
     for (int i = 0; i < kBars; ++i) mbar_init(bar + i, count[i]);
     *abort = 0;
     mbar_fence_init();
@@ -131,12 +127,19 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
   umma::fence_after_sync();
   const uint32_t tm = *tm_slot;
   const long long lim = a.wait_limit;
+  grid_wait();
+  grid_launch_next();
+  PrefillSeq q;
+  int h, *s_item = reinterpret_cast<int *>(smem + kOffBar + kBars * 8 + 12);
+  auto next = [&]() { return next_item<kThreadsG, kBars>(a, bar, count, s_item, abort, q, h); };
 
   if (warp < 8) {
     // -------------------------------------------------------- the chain
     more_registers<kRegsChain>();
     const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    while (next()) {
+    const int chunks = (q.n + kT - 1) / kT;
     float S[64];
     if (q.src < 0) {
 #pragma unroll
@@ -248,6 +251,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
 #pragma unroll
       for (int c = 0; c < 64; c += 8) st_sector(dst + c, S + c);
     }
+    }
   } else if (warp < 16) {
     // ------------------------------- A, M, T and the outputs of every second chunk
     fewer_registers<kRegsIntra>();
@@ -258,6 +262,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     float *sTa = reinterpret_cast<float *>(smem + kOffTa + me4 * kScratch);
     float *sTb = reinterpret_cast<float *>(smem + kOffTb + me4 * kScratch);
     float *sX = reinterpret_cast<float *>(smem + kOffX + me4 * kScratch);
+    while (next()) {
+    const int chunks = (q.n + kT - 1) / kT;
     for (int i = me4; i < chunks; i += 2) {
       const int buf = me4;
       const Scalars &sc = scs[buf];
@@ -418,6 +424,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       }
       warp_arrive(bar + kScFree0 + buf);
     }
+    }
   } else if (warp == 16) {
     // -------------------------------------------------------- the products
     fewer_registers<kRegsRest>();
@@ -463,9 +470,11 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       }
       __syncwarp();
     };
-    bool good = chunks == 0 || warp_wait(bar + kFull0, 0, abort, lim);
+    while (next()) {
+    const int chunks = (q.n + kT - 1) / kT;
+    bool good = warp_wait(bar + kFull0, 0, abort, lim);
     umma::fence_after_sync();
-    if (good && chunks > 0) gram(0);
+    if (good) gram(0);
     for (int i = 0; good && i < chunks; ++i) {
       const uint32_t ph = i & 1;
       const uint32_t kq = base + kOffKQ + (i & 1) * 2 * kBlk;
@@ -506,9 +515,15 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       }
       __syncwarp();
     }
+    // the arrivals that nobody else waits for, before the barriers start anew
+    for (int i = chunks > 1 ? chunks - 2 : 0; good && i < chunks; ++i)
+      warp_wait(bar + kStage0 + (i & 1), (i >> 1) & 1, abort, lim);
+    }
   } else if (warp == 17) {
     // -------------------------------------------------------- decays
     fewer_registers<kRegsRest>();
+    while (next()) {
+    const int chunks = (q.n + kT - 1) / kT;
     const float *pa = static_cast<const float *>(a.in[3]) + h, *pb = static_cast<const float *>(a.in[4]) + h;
     auto load = [&](int i, float (&al)[2], float (&be)[2]) {
 #pragma unroll
@@ -553,10 +568,13 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       if (lane == 0) sc.last = ex2((float)last);
       warp_arrive(bar + kScFull0 + (i & 1));
     }
+    }
   } else {
     // -------------------------------------------------------- tiles
     fewer_registers<kRegsRest>();
     const int l = t - 576;   // 0..63
+    while (next()) {
+    const int chunks = (q.n + kT - 1) / kT;
     const __nv_bfloat16 *in[3];
 #pragma unroll
     for (int k = 0; k < 3; ++k) in[k] = static_cast<const __nv_bfloat16 *>(a.in[k]) + (size_t)h * kD;
@@ -579,6 +597,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       mbar_arrive(bar + kFull0 + st);
     }
     cp_async_wait_all();
+    }
   }
   // -------------------------------------------------------- end
   __syncwarp();
@@ -607,8 +626,8 @@ bool gdn_chunk_path(const PrefillArgs &a, int in_dtype) {
 cudaError_t gdn_chunk_prefill(const PrefillArgs &a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemG);
   if (e != cudaSuccess) return e;
-  gdn_chunk_kernel<<<(unsigned)((size_t)a.n_seq * a.H), kThreadsG, kSmemG, s>>>(a);
-  return cudaGetLastError();
+  const size_t items = (size_t)a.n_seq * a.H;
+  return launch_early(gdn_chunk_kernel, (unsigned)(items < kPrefillSms ? items : kPrefillSms), kThreadsG, kSmemG, s, a);
 }
 
 }  // namespace rssm

@@ -58,19 +58,15 @@ constexpr int kTmCb = 0, kTmY = 128, kTmC = 192, kTmU = 256, kTmL = 320;
 template <int N>
 __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  const PrefillSeq q = a.seqs[blockIdx.x / a.H];
-  if (q.dst < 0) return;
-  const int h = (int)(blockIdx.x % a.H);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int chunks = (q.n + kT - 1) / kT;
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kOffBar);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + kOffBar + kBars * 8);
   uint32_t *tm_slot = reinterpret_cast<uint32_t *>(smem + kOffBar + kBars * 8 + 8);
   float *s_last = reinterpret_cast<float *>(smem + kOffBar + kBars * 8 + 16);   // e^{G_last}
   float4 *sc = reinterpret_cast<float4 *>(smem + kOffSc);
   const uint32_t base = smem_u32(smem);
+  constexpr int count[kBars] = {128, 128, 8, 1, 1, 8, 1, 1, 8, 8, 8, 8, 8, 8, 1, 16, 8, 8, 1};
   if (t == 0) {
-    const int count[kBars] = {128, 128, 8, 1, 1, 8, 1, 1, 8, 8, 8, 8, 8, 8, 1, 16, 8, 8, 1};
     for (int i = 0; i < kBars; ++i) mbar_init(bar + i, count[i]);
     *abort = 0;
     mbar_fence_init();
@@ -93,8 +89,11 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
   umma::fence_after_sync();
   const uint32_t tm = *tm_slot;
   const long long lim = a.wait_limit;
-  const float *src = a.hc + ((size_t)(q.src < 0 ? 0 : q.src) * a.H + h) * kP * N;
-  float *dst = a.hc + ((size_t)q.dst * a.H + h) * kP * N;
+  grid_wait();
+  grid_launch_next();
+  PrefillSeq q;
+  int h, *s_item = reinterpret_cast<int *>(smem + kOffBar + kBars * 8 + 12);
+  auto next = [&]() { return next_item<kThreadsM, kBars>(a, bar, count, s_item, abort, q, h); };
 
   if (warp < 8) {
     // ------------------------------------------------ L, and the outputs
@@ -106,6 +105,8 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       for (int cb = w + 1; cb < 4; ++cb)   // above the diagonal L stays zero
         for (int p = 0; p < 3; ++p) st_x8(lanes + kTmL + p * 64 + cb * 16 + wg * 8, z);
     }
+    while (next()) {
+    const int chunks = (q.n + kT - 1) / kT;
     const float Dh = __ldg(a.D + h);
     for (int i = 0; i < chunks; ++i) {
       const uint32_t ph = i & 1;
@@ -201,10 +202,15 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
         if (first + k * 4 < q.n) st_stream(o, z[k]);
       warp_arrive(bar + kXfree);
     }
+    }
   } else if (warp < 16) {
     // ------------------------------------------------ the state
     const int u = t - 256, wg = (warp - 8) >> 2, n = (warp & 3) * 32 + lane, p0 = wg * 32;
     const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    while (next()) {
+    const int chunks = (q.n + kT - 1) / kT;
+    const float *src = a.hc + ((size_t)(q.src < 0 ? 0 : q.src) * a.H + h) * kP * N;
+    float *dst = a.hc + ((size_t)q.dst * a.H + h) * kP * N;
     float S[32];
 #pragma unroll
     for (int p = 0; p < 32; ++p) S[p] = q.src < 0 || n >= N ? 0.f : __ldcs(src + (size_t)(p0 + p) * N + n);
@@ -283,11 +289,14 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
     if (good && n < N)
 #pragma unroll
       for (int p = 0; p < 32; ++p) dst[(size_t)(p0 + p) * N + n] = S[p];
+    }
   } else if (warp == 16) {
     // ------------------------------------------------ the products
     constexpr int KN = N / 16;   // K steps along n
     // sums run from the small parts of a split to the large: the tensor core truncates
     // each addition, and only those of the last, large part then count
+    while (next()) {
+    const int chunks = (q.n + kT - 1) / kT;
     for (int i = 0; i < chunks; ++i) {
       const uint32_t ph = i & 1;
       const uint32_t Bt = base + kOffB + (i & 1) * 2 * kBlk, Xt = base + kOffX + (i & 1) * kBlk;
@@ -346,8 +355,11 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       if (elect_one()) umma::commit(bar + kIntra);
       __syncwarp();
     }
+    }
   } else if (warp == 17) {
     // ------------------------------------------------ decays
+    while (next()) {
+    const int chunks = (q.n + kT - 1) / kT;
     const double Ah = (double)__ldg(a.A + h) * 1.4426950408889634;   // in powers of two
     const __nv_bfloat16 *pdt = static_cast<const __nv_bfloat16 *>(a.in[3]) + h;
     auto load = [&](int i, float (&v)[4]) {
@@ -393,9 +405,12 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       if (lane == 0) *s_last = ex2((float)last);
       warp_arrive(bar + kScFull);
     }
+    }
   } else {
     // ------------------------------------------------ tiles
     const int l = t - 576;   // 0..127
+    while (next()) {
+    const int chunks = (q.n + kT - 1) / kT;
     const int g = h / a.hpg;
     const __nv_bfloat16 *px = static_cast<const __nv_bfloat16 *>(a.in[0]) + (size_t)h * kP;
     const __nv_bfloat16 *pB = static_cast<const __nv_bfloat16 *>(a.in[1]) + (size_t)g * N;
@@ -422,6 +437,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       mbar_arrive(bar + kFull0 + st);
     }
     cp_async_wait_all();
+    }
   }
   // ------------------------------------------------ end
   __syncwarp();
@@ -451,8 +467,8 @@ cudaError_t m2_chunk_prefill(const PrefillArgs &a, cudaStream_t s) {
   auto kernel = a.C == 64 ? m2_chunk_kernel<64> : m2_chunk_kernel<128>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemM);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)((size_t)a.n_seq * a.H), kThreadsM, kSmemM, s>>>(a);
-  return cudaGetLastError();
+  const size_t items = (size_t)a.n_seq * a.H;
+  return launch_early(kernel, (unsigned)(items < kPrefillSms ? items : kPrefillSms), kThreadsM, kSmemM, s, a);
 }
 
 }  // namespace rssm

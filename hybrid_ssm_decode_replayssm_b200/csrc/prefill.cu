@@ -5,6 +5,7 @@
 //   scan_kernel           four tokens at a time, the state in registers
 //   requantize_kernel     the read copies of the rows written
 #include "rssm_prefill.h"
+#include "chunk.cuh"
 #include "slots.cuh"
 
 namespace rssm {
@@ -21,8 +22,10 @@ constexpr int kPlanThreads = 1024;
 
 __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const PrefillArgs a) {
   const int nt = blockDim.x, t = threadIdx.x;
+  chunk::grid_launch_next();   // the kernels behind wait for this grid themselves
   if (a.slot) adopt_folds(a.B, a.slot, a.dst, a.seen, a.flushes);
   for (int b = t; b < a.B; b += nt) a.named[b] = 0;
+  if (t < kCounters + kSmCounters) a.queue[t] = 0;
   bool bad = false;
   for (int i = t; i < a.n_seq; i += nt) {
     const int o0 = a.offsets[i], o1 = a.offsets[i + 1];
@@ -81,15 +84,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
       q.src = src;
       q.dst = to;
       a.seqs[place] = q;
+      if (n > a.scan_most) atomicMax(a.queue + kLongCount, place + 1);
     }
     rank += tot;
   }
 }
 
 // -------------------------------------------------------- four tokens at a time
-// One CTA of 256 threads per (sequence, head, 64 state rows): four warps run the
-// recurrence, the state in registers (16 columns of four rows per thread, two at dstate
-// 64, as packed pairs); four warps bring the tokens, eight at a time, as fp32 into two buffers of
+// One CTA of 256 threads per (sequence, head, 32 or 64 state rows): four warps run the
+// recurrence, the state in registers (16 columns of one to four rows per thread, as
+// packed pairs); four warps bring the tokens, eight at a time, as fp32 into two buffers of
 // shared memory, with what depends on the tokens alone, and take the outputs away.
 // Four tokens i = 0..3 go together: with p_i the product of their gates up to i and
 // d_ij that of the gates j+1..i (products, never ratios),
@@ -102,9 +106,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
 // no u, w = dt x.  KDA: one gate per channel, so p and d go into the vectors (p_i k_i,
 // p_i q_i, d_3j k_j).  Bound by the CUDA cores' issue and the round's latency.
 constexpr int kScanThreads = 256;
-constexpr int kScanRows = 64;
 constexpr int kScanTok = 8;    // tokens per buffer: two blocks of four
-constexpr int kScanOcc = 4;    // CTAs per SM of the grid at most
+// registers per thread: 128 x 184 + 128 x 72 = 256 x 128, so that two CTAs fit
+constexpr int kScanRegs = 184, kBringRegs = 72;
 
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 pack2(float x, float y) {
@@ -154,40 +158,65 @@ struct __align__(16) ScanBlock {
   float pc, pad[3];
 };
 
-template <int KIND, typename Tin, int C>
-__global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const PrefillArgs a, int items) {
+template <int KIND, typename Tin, int C, int ROWS>
+__global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs a, int items, bool behind_chunks) {
   constexpr bool M2 = KIND == RSSM_MAMBA2, KDA = KIND == RSSM_KDA;
   constexpr int LPR = C / 16;                       // lanes per row
   constexpr int GROUPS = 128 / LPR;                 // rows per pass: 16 or 32
-  constexpr int RPT = kScanRows / GROUPS;           // rows per thread: 4 or 2
+  constexpr int RPT = ROWS / GROUPS;                // rows per thread
   constexpr int NV = RPT * 4;                       // a thread's sums for four tokens
-  static_assert(NV == 2 * LPR, "of which it keeps two");
+  constexpr int PL = NV / LPR, LR = 4 / PL;         // the sums it keeps; lanes that hold a row's four
+  static_assert(PL == 1 || PL == 2, "sums per lane");
   struct Buf {
     float k[kScanTok][C], q[kScanTok][C];           // KDA: p_i k_i, p_i q_i
     float kt[KDA ? kScanTok : 1][C], pc[KDA ? 2 : 1][C];   // KDA: d_3j k_j, p_3
-    float v[kScanTok][kScanRows], o[kScanTok][kScanRows];
+    float v[kScanTok][ROWS], o[kScanTok][ROWS];
     ScanBlock blk[2];
   };
   __shared__ __align__(16) Buf buf[2];
   __shared__ __align__(16) float raw_k[KDA ? kScanTok : 1][C], raw_g[KDA ? kScanTok : 1][C];
   __shared__ __align__(16) float s_gate[kScanTok], s_beta[kScanTok];
-  const int slices = a.R / kScanRows;
+  __shared__ int s_item;
+  const int slices = a.R / ROWS;
+  // alone, this grid waits for the planner's; behind a chunked kernel, whose CTAs have all
+  // waited for it, it runs beside them and waits for their end before its own
+  if (!behind_chunks) chunk::grid_wait();
+  const int first = a.queue[kLongCount] * a.H * slices;
   const int t = threadIdx.x, lane = t & 31;
   const size_t tile = (size_t)a.R * C;
-  // barriers: 1, 2 a buffer is full; 3, 4 it is empty; 5 the bringing warps among themselves
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int h = item % a.H, sl = item / a.H % slices;
-    const PrefillSeq q = a.seqs[item / a.H / slices];
-    if (q.dst < 0 || q.n > a.scan_most) continue;
-    const int tiles = (q.n + kScanTok - 1) / kScanTok;
-    if (t < 128) {
-      // ------------------------------------------------ the recurrence
+  // barriers: 1, 2 a buffer is full; 3, 4 it is empty; 5 the bringing warps among themselves;
+  // 6, 7 the begin and the end of an item
+  if (t < 128) {
+    // -------------------------------------------------- the recurrence
+    chunk::more_registers<kScanRegs>();
+    // items in turn: an SM's first CTA takes the longest one left, its second the shortest,
+    // so that long sequences do not share an SM (which CTA runs an item changes nothing in it)
+    uint32_t sm;
+    asm volatile("mov.u32 %0, %smid;" : "=r"(sm));
+    const bool front = t != 0 || sm >= kSmCounters || atomicAdd(a.queue + kCounters + sm, 1) == 0;
+    for (;;) {
+      if (t == 0) {
+        const bool any = atomicAdd(a.queue + kScanTaken, 1) < items - first;
+        s_item = !any ? items
+                      : front ? first + atomicAdd(a.queue + kScanFront, 1)
+                              : items - 1 - atomicAdd(a.queue + kScanBack, 1);
+      }
+      named_sync(6, kScanThreads);
+      const int item = s_item;
+      if (item >= items) break;
+      const int h = item % a.H, sl = item / a.H % slices;
+      const PrefillSeq q = a.seqs[item / a.H / slices];
+      if (q.dst < 0 || q.n > a.scan_most) {
+        named_sync(7, kScanThreads);
+        continue;
+      }
+      const int tiles = (q.n + kScanTok - 1) / kScanTok;
       const int sub = t % LPR, grp = t / LPR, lane0 = lane - sub;
-      const int mine = grp + sub / 2 * GROUPS, i0 = sub % 2 * 2;   // the row and tokens whose sums this lane keeps
+      const int mine = grp + sub / LR * GROUPS, i0 = sub % LR * PL;   // the row and tokens whose sums this lane keeps
       f32x2 S[RPT][8];
 #pragma unroll
       for (int r = 0; r < RPT; ++r) {
-        const int row = sl * kScanRows + grp + r * GROUPS;
+        const int row = sl * ROWS + grp + r * GROUPS;
         const float *src = a.hc + ((size_t)(q.src < 0 ? 0 : q.src) * a.H + h) * tile + (size_t)row * C;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -207,8 +236,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const PrefillArgs
           const float4 be = *reinterpret_cast<const float4 *>(K.be);
           float w[4] = {be.x * B.v[b * 4][mine], be.y * B.v[b * 4 + 1][mine], be.z * B.v[b * 4 + 2][mine],
                         be.w * B.v[b * 4 + 3][mine]};
-          // sums[0], sums[1]: S x_i of row mine and tokens i0, i0 + 1 (whole, over the lanes)
-          float u[M2 ? 2 : NV], z[NV];
+          float u[M2 ? 1 : NV], z[NV];   // S k_i and S q_i
           {
             f32x2 au[M2 ? 1 : NV], az[NV];
 #pragma unroll
@@ -240,8 +268,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const PrefillArgs
           if constexpr (!M2) tr_sum<NV, LPR / 2>(u, lane);
           tr_sum<NV, LPR / 2>(z, lane);
           if constexpr (!M2) {
-            const float x0 = __shfl_xor_sync(kFull, u[0], 1), x1 = __shfl_xor_sync(kFull, u[1], 1);
-            const float u4[4] = {i0 ? x0 : u[0], i0 ? x1 : u[1], i0 ? u[0] : x0, i0 ? u[1] : x1};
+            float u4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u4[i] = __shfl_sync(kFull, u[i % PL], lane - sub % LR + i / PL);
             const float4 bg = *reinterpret_cast<const float4 *>(K.bg);
             const float4 a1 = *reinterpret_cast<const float4 *>(K.A[1]), a2 = *reinterpret_cast<const float4 *>(K.A[2]);
             const float4 a3 = *reinterpret_cast<const float4 *>(K.A[3]);
@@ -258,12 +287,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const PrefillArgs
             const float own = KDA ? w[j] : fs[j] * w[j];
 #pragma unroll
             for (int r = 0; r < RPT; ++r) {
-              const float x = __shfl_sync(kFull, own, lane0 + 2 * r);
+              const float x = __shfl_sync(kFull, own, lane0 + LR * r);
               fw[r][j] = pack2(x, x);
             }
           }
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {   // the outputs of this lane's row and tokens
+          for (int s = 0; s < PL; ++s) {   // the outputs of this lane's row and tokens
             const int i = i0 + s;
             const float4 m = *reinterpret_cast<const float4 *>(K.M[i]);
             const float o = fmaf(m.x, w[0], fmaf(m.y, w[1], fmaf(m.z, w[2], fmaf(m.w, w[3], K.p[i] * z[s]))));
@@ -296,26 +325,40 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const PrefillArgs
       }
 #pragma unroll
       for (int r = 0; r < RPT; ++r) {
-        const int row = sl * kScanRows + grp + r * GROUPS;
+        const int row = sl * ROWS + grp + r * GROUPS;
         float *dst = a.hc + ((size_t)q.dst * a.H + h) * tile + (size_t)row * C;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           *reinterpret_cast<ulonglong2 *>(dst + c * (C / 4) + sub * 4) = make_ulonglong2(S[r][2 * c], S[r][2 * c + 1]);
       }
-    } else {
-      // ------------------------------------------------ tokens in, outputs out
+      named_sync(7, kScanThreads);   // the buffers and barriers start anew
+    }
+  } else {
+    // -------------------------------------------------- tokens in, outputs out
+    chunk::fewer_registers<kBringRegs>();
+    for (;;) {
+      named_sync(6, kScanThreads);
+      const int item = s_item;
+      if (item >= items) break;
+      const int h = item % a.H, sl = item / a.H % slices;
+      const PrefillSeq q = a.seqs[item / a.H / slices];
+      if (q.dst < 0 || q.n > a.scan_most) {
+        named_sync(7, kScanThreads);
+        continue;
+      }
+      const int tiles = (q.n + kScanTok - 1) / kScanTok;
       const int l = t - 128;
       const int hk = M2 ? h / a.hpg : h;                 // head (or group) of k and q
       const Tin *pk = static_cast<const Tin *>(a.in[1]) + (size_t)hk * C;
       const Tin *pq = static_cast<const Tin *>(a.in[M2 ? 2 : 0]) + (size_t)hk * C;
-      const Tin *pv = static_cast<const Tin *>(a.in[M2 ? 0 : 2]) + (size_t)h * a.R + sl * kScanRows;
+      const Tin *pv = static_cast<const Tin *>(a.in[M2 ? 0 : 2]) + (size_t)h * a.R + sl * ROWS;
       const int64_t dk = a.stride[1], dq = a.stride[M2 ? 2 : 0], dv = a.stride[M2 ? 0 : 2];
       const float Ah = M2 ? __ldg(a.A + h) : 0.f;
       const float scale = M2 ? 1.f : a.out_scale;
       constexpr int per = C / 8;                         // threads per token: 16 or 8
       const int e = l / per, c8 = l % per * 8;           // this thread's token and columns
       const int bi = e & 3, bb = e & ~3;                 // its place in its block, and the block's first
-      const int ve = l / 16, vc = l % 16 * 4;            // and its four values of v
+      const int ve = l / (ROWS / 4), vc = l % (ROWS / 4) * 4;   // and its four values of v
       float k8[8], q8[8], g8[8];
       // the next tile's values as they come: widened only when they are used, so that
       // nothing waits for them before
@@ -351,7 +394,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const PrefillArgs
             }
           }
         }
-        if (ve < m) {
+        if (ve < m && ve < kScanTok) {
           const Tin *p = pv + (tok + ve) * dv + vc;
           if constexpr (sizeof(Tin) == 4) {
             rv = __ldg(reinterpret_cast<const uint4 *>(p));
@@ -368,8 +411,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const PrefillArgs
       };
       auto flush = [&](int n) {   // the outputs of tile n
         const int64_t tok = (int64_t)q.tok + n * kScanTok;
-        if (ve < q.n - n * kScanTok)
-          st_stream(a.out + ((tok + ve) * a.H + h) * a.R + sl * kScanRows + vc,
+        if (ve < kScanTok && ve < q.n - n * kScanTok)
+          st_stream(a.out + ((tok + ve) * a.H + h) * a.R + sl * ROWS + vc,
                     *reinterpret_cast<const float4 *>(&buf[n & 1].o[ve][vc]));
       };
       if (tiles > 0) load(0);
@@ -409,7 +452,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const PrefillArgs
           else
             x = make_float4(__uint_as_float(rv.x << 16), __uint_as_float(rv.x & 0xFFFF0000u), __uint_as_float(rv.y << 16),
                             __uint_as_float(rv.y & 0xFFFF0000u));
-          *reinterpret_cast<float4 *>(&B.v[ve][vc]) = x;
+          if (ve < kScanTok) *reinterpret_cast<float4 *>(&B.v[ve][vc]) = x;
         }
         if (n + 1 < tiles) load(n + 1);
         named_sync(5, 128);
@@ -478,9 +521,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_kernel(const PrefillArgs
         named_sync(3 + (n & 1), kScanThreads);
         flush(n);
       }
+      named_sync(7, kScanThreads);
     }
-    __syncthreads();   // the buffers and barriers start anew
   }
+  if (behind_chunks) chunk::grid_wait();
 }
 
 // ------------------------------------------------------------- read copies
@@ -500,54 +544,68 @@ __global__ void __launch_bounds__(256) requantize_kernel(const PrefillArgs a) {
   }
 }
 
-template <int KIND, typename Tin>
-void launch_scan(const PrefillArgs &a, cudaStream_t s) {
-  const int items = (int)((size_t)a.n_seq * a.H * (a.R / kScanRows));
-  const dim3 grid((unsigned)(items < 148 * kScanOcc ? items : 148 * kScanOcc));
-  if constexpr (KIND == RSSM_MAMBA2)
-    if (a.C == 64) {
-      scan_kernel<KIND, Tin, 64><<<grid, kScanThreads, 0, s>>>(a, items);
-      return;
-    }
-  scan_kernel<KIND, Tin, 128><<<grid, kScanThreads, 0, s>>>(a, items);
+template <int KIND, typename Tin, int C, int ROWS>
+cudaError_t launch_scan_rows(const PrefillArgs &a, bool behind_chunks, cudaStream_t s) {
+  const int items = (int)((size_t)a.n_seq * a.H * (a.R / ROWS));
+  const int most = kPrefillSms * 2;
+  return launch_early(scan_kernel<KIND, Tin, C, ROWS>, (unsigned)(items < most ? items : most), kScanThreads, 0, s, a,
+                      items, behind_chunks);
 }
 
-constexpr int kScanMean = 0;
+template <int KIND, typename Tin>
+cudaError_t launch_scan(const PrefillArgs &a, bool behind_chunks, cudaStream_t s) {
+  // 32 rows per CTA while every CTA then has an SM of its own (0.18 us per token against
+  // 0.25, GDN); otherwise 64, which read the tokens half as often (32 sequences of 128
+  // tokens, 32 heads: 386 us against 584)
+  const bool fine = (long long)a.n_seq * a.H * a.R <= (long long)kPrefillSms * 32;
+  if constexpr (KIND == RSSM_MAMBA2)
+    if (a.C == 64)
+      return fine ? launch_scan_rows<KIND, Tin, 64, 32>(a, behind_chunks, s)
+                  : launch_scan_rows<KIND, Tin, 64, 64>(a, behind_chunks, s);
+  return fine ? launch_scan_rows<KIND, Tin, 128, 32>(a, behind_chunks, s)
+              : launch_scan_rows<KIND, Tin, 128, 64>(a, behind_chunks, s);
+}
+
+// Sequences of up to this many tokens run four tokens at a time even where a chunked kernel
+// serves the layer, whose first chunk costs as much as a full one.
+constexpr int kScanMost = 24;
 
 size_t seq_bytes(int n_seq) { return ((size_t)n_seq * sizeof(PrefillSeq) + 255) & ~(size_t)255; }
 
 }  // namespace
 
 size_t prefill_work_bytes(const rssm_layer_desc &d, int n_seq, int n_tokens) {
-  return seq_bytes(n_seq) + (size_t)d.batch * sizeof(int32_t);
+  return seq_bytes(n_seq) + (kCounters + kSmCounters + (size_t)d.batch) * sizeof(int32_t);
 }
 
 cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *launches, cudaStream_t s) {
   a.seqs = static_cast<PrefillSeq *>(work);
-  a.named = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(work) + seq_bytes(a.n_seq));
+  a.queue = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(work) + seq_bytes(a.n_seq));
+  a.named = a.queue + kCounters + kSmCounters;
   *launches = 0;
+  const bool m2_chunks = m2_chunk_path(a, in_dtype), gdn_chunks = gdn_chunk_path(a, in_dtype);
+  const bool chunks = (m2_chunks || gdn_chunks) && a.n_tokens > kScanMost;
+  a.scan_most = chunks ? kScanMost : a.n_tokens;
   plan_prefill_kernel<<<1, kPlanThreads, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   ++*launches;
   if (e != cudaSuccess) return e;
-  a.scan_most = a.n_tokens;
+  if (chunks) {
+    e = m2_chunks ? m2_chunk_prefill(a, s) : gdn_chunk_prefill(a, s);
+    ++*launches;
+    if (e != cudaSuccess) return e;
+  }
   const bool bf16 = in_dtype == RSSM_BF16;
-  const bool few = a.n_tokens <= (long long)kScanMean * a.n_seq;
-  if (!few && m2_chunk_path(a, in_dtype))
-    e = m2_chunk_prefill(a, s);
-  else if (!few && gdn_chunk_path(a, in_dtype))
-    e = gdn_chunk_prefill(a, s);
-  else switch (a.kind) {
+  switch (a.kind) {
     case RSSM_MAMBA2:
-      bf16 ? launch_scan<RSSM_MAMBA2, __nv_bfloat16>(a, s) : launch_scan<RSSM_MAMBA2, float>(a, s);
+      e = bf16 ? launch_scan<RSSM_MAMBA2, __nv_bfloat16>(a, chunks, s) : launch_scan<RSSM_MAMBA2, float>(a, chunks, s);
       break;
     case RSSM_GDN:
-      bf16 ? launch_scan<RSSM_GDN, __nv_bfloat16>(a, s) : launch_scan<RSSM_GDN, float>(a, s);
+      e = bf16 ? launch_scan<RSSM_GDN, __nv_bfloat16>(a, chunks, s) : launch_scan<RSSM_GDN, float>(a, chunks, s);
       break;
     default:
-      bf16 ? launch_scan<RSSM_KDA, __nv_bfloat16>(a, s) : launch_scan<RSSM_KDA, float>(a, s);
+      e = bf16 ? launch_scan<RSSM_KDA, __nv_bfloat16>(a, chunks, s) : launch_scan<RSSM_KDA, float>(a, chunks, s);
   }
-  if (e == cudaSuccess) e = cudaGetLastError();
   ++*launches;
   if (e != cudaSuccess || read_fmt == RSSM_READ_FP32) return e;
   const dim3 grid((unsigned)((size_t)a.n_seq * a.H));

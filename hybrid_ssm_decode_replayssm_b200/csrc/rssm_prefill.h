@@ -13,6 +13,12 @@ struct PrefillSeq {
   int32_t tok, n, src, dst;
 };
 
+// Counters in the workspace: three of the token scan's items, one of the chunked
+// kernels', the number of sequences up to the last long one; then CTAs begun per SM.
+enum { kScanTaken = 0, kScanFront, kScanBack, kChunkQueue, kLongCount, kCounters };
+constexpr int kSmCounters = 256 - kCounters;
+constexpr int kPrefillSms = 148;   // CTAs of the persistent kernels, one per SM
+
 struct PrefillArgs {
   int kind;
   int B, H, G, hpg, R, C;
@@ -25,8 +31,9 @@ struct PrefillArgs {
   int64_t stride[5];          // elements between consecutive tokens
   float *out;
   const int32_t *offsets, *rows, *fresh;
-  // workspace: the planned sequences, longest first, and a counter per row
+  // workspace: the planned sequences, longest first, work counters, and a counter per row
   PrefillSeq *seqs;
+  int32_t *queue;
   int32_t *named;
   // bookkeeping
   int32_t *len, *pending, *flushes;
@@ -45,11 +52,28 @@ cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *
 
 // The chunked Mamba-2 scan (m2_prefill.cu): bf16 inputs, headdim 64.
 bool m2_chunk_path(const PrefillArgs &a, int in_dtype);
-cudaError_t m2_chunk_prefill(const PrefillArgs &a, cudaStream_t s);
+cudaError_t m2_chunk_prefill(const PrefillArgs &a, cudaStream_t s);   // sequences longer than a.scan_most
 
 // The chunked gated delta rule (gdn_prefill.cu): GDN, bf16 inputs.
 bool gdn_chunk_path(const PrefillArgs &a, int in_dtype);
 cudaError_t gdn_chunk_prefill(const PrefillArgs &a, cudaStream_t s);
+
+// Launch with programmatic stream serialisation: the kernel may begin before the grid
+// ahead of it ends, and waits for it itself.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
 
 // One side of a row move: the buffers of a layer.
 struct RowsSide {
