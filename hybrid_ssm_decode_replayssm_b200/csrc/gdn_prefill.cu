@@ -14,15 +14,15 @@
 //   W^T = R^T T^T           six (both sides split; the parts below 2^-24 left out)
 //   O^T = W^T M^T           six
 //   S' += (fw W)^T K        three
-// so states and outputs keep fp32 accuracy.  [K; Q] K^T gives A and M; T is made from
-// A in fp32 by one warpgroup, a chunk ahead of its use.
+// so states and outputs keep fp32 accuracy.  [K; Q] K^T gives A and M; T comes
+// from a kernel of its own before (gdn_pre_kernel), which has no chain to wait for.
 // Far decays are differences of double prefix sums kept as two floats.
 //
 // Bound by the chain S -> U -> R -> W -> S' of one chunk after the other.
 //
 // Roles: warps 0-7 the chain (one value row per lane, two halves of the columns),
-// warps 8-11 and 12-15 A, M, T and the outputs of every second chunk, warp 16 issues
-// the products, warp 17 the decays, warps 18-19 load the tiles with zeros behind the sequence's end.
+// warps 8-11 and 12-15 M and the outputs of every second chunk, warp 16 issues
+// the products, warps 18-19 load the tiles with zeros behind the sequence's end.
 #include "chunk.cuh"
 #include "rssm_prefill.h"
 
@@ -36,22 +36,17 @@ constexpr int kD = 128;
 constexpr int kBlk = 16384;                 // 128 rows x 64 bf16
 constexpr int kPart = 8192;                 // 64 x 64 bf16
 constexpr int kThreadsG = 640;
-// registers per thread: 256 x 120 + 256 x 88 + 128 x 64 = 640 x 96
-constexpr int kRegsLaunch = 96, kRegsChain = 120, kRegsIntra = 88, kRegsRest = 64;
-static_assert(256 * kRegsChain + 256 * kRegsIntra + 128 * kRegsRest <= kThreadsG * kRegsLaunch, "registers of the CTA");
+// registers per thread: 256 x 128 + 256 x 80 + 128 x 64 = 640 x 96
+constexpr int kRegsLaunch = 96, kRegsChain = 128, kRegsOut = 80, kRegsRest = 64;
+static_assert(256 * kRegsChain + 256 * kRegsOut + 128 * kRegsRest <= kThreadsG * kRegsLaunch, "registers of the CTA");
 constexpr int kALd = 68, kTLd = 36, kXLd = 20;   // floats per row of A^T, of 32-wide and of 16-wide blocks
 // shared memory
 constexpr int kOffKQ = 0;                   // two stages: rows 0-63 K, 64-127 Q, two column blocks
 constexpr int kOffV = 4 * kBlk;             // two stages [t][dv]
 constexpr int kOffT = kOffV + 2 * kBlk;     // two buffers of three parts, [t][s]
 constexpr int kOffM = kOffT + 6 * kPart;
-constexpr int kOffTa = kOffM + 6 * kPart;          // two of: T's first 32 rows and columns, [row][column]
-constexpr int kOffTb = kOffTa + 32 * kTLd * 4;     //   its last 32, [column][row]
-constexpr int kOffX = kOffTb + 32 * kTLd * 4;      //   blocks on the way
-constexpr int kScratch = 2 * 32 * kTLd * 4 + 4 * 16 * kXLd * 4;
-constexpr int kOffSc = kOffTa + 2 * kScratch;
-static_assert(kT * kALd * 4 <= 3 * kPart, "A^T (fp32, [s][t]) lies where T's parts go");
-struct Scalars {
+constexpr int kOffSc = kOffM + 6 * kPart;
+struct Scalars {        // of a chunk, made with its T
   float2 g[kT];        // G as two floats, in powers of two
   float be[kT];        // b_t
   float bg[kT];        // b_t e^{G_t}
@@ -59,11 +54,15 @@ struct Scalars {
   float fw[kT];        // e^{G_last - G_t}
   float last, pad[3];  // e^{G_last}
 };
-constexpr int kOffBar = kOffSc + 2 * (int)sizeof(Scalars);
-enum { kFull0 = 0, kFull1, kStage0, kStage1, kScFull0, kScFull1, kScFree0, kScFree1, kA0, kA1, kTm0, kTm1, kO0, kO1,
+constexpr int kRecord = 3 * kPart + 2048;   // a chunk and head in the workspace: T's parts, the scalars
+static_assert(sizeof(Scalars) % 16 == 0 && sizeof(Scalars) <= 2048, "record");
+// four places for scalars: those of chunk i are read by its outputs, and chunk i + 4 comes
+// after the update of chunk i + 2, which the same warps' outputs precede
+constexpr int kOffBar = kOffSc + 4 * (int)sizeof(Scalars);
+enum { kFull0 = 0, kFull1, kStage0, kStage1, kA0, kA1, kM0, kM1, kO0, kO1,
        kSp0, kSp1, kU, kQ, kRp, kW, kWp, kFwp, kUpd, kOfree, kAfree, kDrain, kBars };
 constexpr int kSmemG = kOffBar + kBars * 8 + 32;
-static_assert(kSmemG <= 232448 && 32 * kTLd <= 4 * 16 * kXLd, "shared memory of one CTA");
+static_assert(kSmemG <= 232448, "shared memory of one CTA");
 // tensor memory columns.  U^T, then W^T, then the masked product; Z^T; the parts of S,
 // then of fw W; the state's update, before it the parts of R, then of W; [K; Q] K^T
 constexpr int kTmU = 0, kTmZ = 64, kTmS = 128, kTmFw = 128, kTmD = 320, kTmR = 320, kTmW = 320, kTmA = 448;
@@ -101,6 +100,235 @@ __device__ __forceinline__ void block_product(float (&o)[4][NC], const float *L,
   }
 }
 
+// T = (I + A)^-1 of every chunk and head of the long sequences, in the three parts and the
+// place of each that the chain's kernel reads: everything that does not wait for a state.
+// One CTA of four warps at a time per (chunk, head), four of them per SM.  K K^T on
+// mma.sync (64 x 64 outputs of exact products; the 5th-generation cores take 128 rows at
+// least, half of them wasted here); T in fp32 by blocks: sixteen-wide diagonal blocks by
+// substitution, one per warp, a column per lane; then T_10 = -T_11 (A_10 T_00) for pairs of
+// blocks, and again for pairs of those.
+constexpr int kPreThreads = 128;
+constexpr int kPreOffA = 2 * kPart;                      // K: two blocks of 64 columns; A^T, [s][t]
+constexpr int kPreOffTa = kPreOffA + kT * kALd * 4;      // T's first 32 rows and columns, [row][column]
+constexpr int kPreOffTb = kPreOffTa + 32 * kTLd * 4;     // its last 32, [column][row]
+constexpr int kPreOffX = kPreOffTb + 32 * kTLd * 4;      // blocks on the way
+constexpr int kPreOffG = kPreOffX + 4 * 16 * kXLd * 4;   // G as two floats, b
+constexpr int kSmemPre = kPreOffG + kT * 12 + 16;
+static_assert(32 * kTLd <= 4 * 16 * kXLd, "the blocks on the way");
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The running sum of the log gates (base 2) of a chunk, two tokens per lane, and its total.
+__device__ __forceinline__ double gate_sums(const float (&al)[2], int lane, double (&G)[2]) {
+  // a gate of 0 forgets all: any power of two this far down does
+  G[0] = fmax(log2((double)al[0]), -16384.0);
+  G[1] = G[0] + fmax(log2((double)al[1]), -16384.0);
+  double inc = G[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  const double before = inc - G[1];
+  G[0] += before;
+  G[1] += before;
+  return __shfl_sync(0xffffffffu, inc, 31);
+}
+
+__global__ void __launch_bounds__(kPreThreads, 4) gdn_pre_kernel(const PrefillArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+  const uint32_t base = smem_u32(smem);
+  float *sA = reinterpret_cast<float *>(smem + kPreOffA), *sTa = reinterpret_cast<float *>(smem + kPreOffTa);
+  float *sTb = reinterpret_cast<float *>(smem + kPreOffTb), *sX = reinterpret_cast<float *>(smem + kPreOffX);
+  float2 *sG = reinterpret_cast<float2 *>(smem + kPreOffG);
+  float *sBe = reinterpret_cast<float *>(smem + kPreOffG + kT * 8);
+  for (int i = t; i < (kPreOffG - kPreOffTa) / 4; i += kPreThreads) sTa[i] = 0.f;   // zero above the diagonal
+  grid_wait();
+  grid_launch_next();
+  const int total = a.queue[kChunkTotal], longs = a.queue[kLongCount];
+  for (size_t id = blockIdx.x; id < (size_t)total * a.H; id += gridDim.x) {
+    const int h = (int)(id % a.H), chunk = (int)(id / a.H);
+    int lo = 0, hi = longs - 1;   // the last sequence that begins at or before this chunk (and is not empty)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.seqs[mid].first <= chunk) lo = mid;
+      else hi = mid - 1;
+    }
+    const PrefillSeq q = a.seqs[lo];
+    const int t0 = (chunk - q.first) * kT, left = q.n - t0;
+    __syncthreads();   // the last item's blocks are read
+    {
+      const __nv_bfloat16 *pk = static_cast<const __nv_bfloat16 *>(a.in[1]) + (size_t)h * kD;
+      const int c = t & 15;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int s = k * 8 + (t >> 4);
+        const bool take = s < left;
+        cp_async16_zfill(base + (c >> 3) * kPart + sw128(s, c & 7),
+                         pk + (int64_t)(q.tok + t0 + (take ? s : 0)) * a.stride[1] + c * 8, take);
+      }
+      cp_commit();
+    }
+    if (w == 0) {
+      const float *pa = static_cast<const float *>(a.in[3]) + h, *pb = static_cast<const float *>(a.in[4]) + h;
+      float al[2], be[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int s = lane * 2 + k;
+        al[k] = s < left ? pa[(int64_t)(q.tok + t0 + s) * a.stride[3]] : 1.f;
+        be[k] = s < left ? pb[(int64_t)(q.tok + t0 + s) * a.stride[4]] : 0.f;
+      }
+      double G[2];
+      const double last = gate_sums(al, lane, G);
+      Scalars &sc = *reinterpret_cast<Scalars *>(a.parts + id * kRecord + 3 * kPart);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int s = lane * 2 + k;
+        const float hi = (float)G[k], e = ex2((float)G[k]);
+        sc.g[s] = sG[s] = make_float2(hi, (float)(G[k] - (double)hi));
+        sc.be[s] = sBe[s] = be[k];
+        sc.bg[s] = be[k] * e;
+        sc.zg[s] = a.out_scale * e;
+        sc.fw[s] = ex2((float)(last - G[k]));
+      }
+      if (lane == 0) sc.last = ex2((float)last);
+    }
+    cp_wait<0>();
+    __syncthreads();
+    {   // rows 16 w .. of K K^T up to the diagonal, then A
+      float acc[4][2][4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[p][n][j] = 0.f;
+      const int ra = w * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, ca = lane >> 4;
+      const int rb = (lane & 7) + ((lane >> 4) & 1) * 8, cb = (lane >> 3) & 1;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        uint32_t fa[4];
+        ldmatrix4(fa, base + (k >> 2) * kPart + sw128(ra, (k & 3) * 2 + ca));
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          if (p <= w) {
+            uint32_t fb[4];
+            ldmatrix4(fb, base + (k >> 2) * kPart + sw128(p * 16 + rb, (k & 3) * 2 + cb));
+            mma_16816(acc[p][0], fa, fb[0], fb[1]);
+            mma_16816(acc[p][1], fa, fb[2], fb[3]);
+          }
+      }
+      const int row = w * 16 + (lane >> 2);
+      const float2 g0 = sG[row], g1 = sG[row + 8];
+      const float b0 = sBe[row], b1 = sBe[row + 8];
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        if (p <= w)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int s = p * 16 + n * 8 + (lane & 3) * 2 + j;
+              const float2 o = sG[s];
+              sA[s * kALd + row] = s < row ? b0 * (ex2((g0.x - o.x) + (g0.y - o.y)) * acc[p][n][j]) : 0.f;
+              sA[s * kALd + row + 8] = s < row + 8 ? b1 * (ex2((g1.x - o.x) + (g1.y - o.y)) * acc[p][n][2 + j]) : 0.f;
+            }
+    }
+    __syncthreads();
+    {
+      const int c = lane & 15;
+      float acc[16], val[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        val[k] = k == c ? 1.f : -acc[k];
+#pragma unroll
+        for (int j = (k + 1) / 4 * 4; j < 16; j += 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(sA + (w * 16 + k) * kALd + w * 16 + j);
+          const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + e > k) acc[j + e] = fmaf(xs[e], val[k], acc[j + e]);
+        }
+      }
+      if (lane < 16) {
+        const int o = (w & 1) * 16;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          if (w < 2) sTa[(o + k) * kTLd + o + c] = val[k];
+          if (w == 1) sX[c * kXLd + k] = val[k];                    // T_11 by columns
+          if (w == 2) sX[(16 + k) * kXLd + c] = val[k];             // T_22 by rows
+        }
+        if (w >= 2) {
+#pragma unroll
+          for (int k = 0; k < 16; k += 4)
+            *reinterpret_cast<float4 *>(sTb + (o + c) * kTLd + o + k) = make_float4(val[k], val[k + 1], val[k + 2], val[k + 3]);
+        }
+      }
+    }
+    __syncthreads();
+    {
+      const int pr = w >> 1, id2 = t & 63, c = id2 & 15, r4 = (id2 >> 4) * 4;
+      float x[4][1];
+      float *sXp = sX + (32 + pr * 16) * kXLd;
+      block_product<1>(x, sA + (pr * 32) * kALd + pr * 32 + 16 + r4, kALd, pr ? sX + 16 * kXLd + c : sTa + c,
+                       pr ? kXLd : kTLd, 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sXp[(r4 + e) * kXLd + c] = x[e][0];
+      __syncthreads();
+      block_product<1>(x, pr ? sTb + 16 * kTLd + 16 + r4 : sX + r4, pr ? kTLd : kXLd, sXp + c, kXLd, 16);
+      if (pr) {
+        *reinterpret_cast<float4 *>(sTb + c * kTLd + 16 + r4) = make_float4(-x[0][0], -x[1][0], -x[2][0], -x[3][0]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sTa[(16 + r4 + e) * kTLd + c] = -x[e][0];
+      }
+    }
+    __syncthreads();
+    {
+      const int c = (t & 15) * 2, r4 = (t >> 4) * 4;
+      uint8_t *to = a.parts + id * kRecord;
+      auto put = [&](int row, int col, float v0, float v1) {
+        uint32_t hi, mid, lo;
+        split3(v0, v1, hi, mid, lo);
+        uint8_t *at = to + sw128(row, col >> 3) + (col & 7) * 2;
+        *reinterpret_cast<uint32_t *>(at) = hi;
+        *reinterpret_cast<uint32_t *>(at + kPart) = mid;
+        *reinterpret_cast<uint32_t *>(at + 2 * kPart) = lo;
+      };
+      float x[4][2];
+      block_product<2>(x, sA + 32 + r4, kALd, sTa + c, kTLd, 32);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) *reinterpret_cast<float2 *>(sX + (r4 + e) * kTLd + c) = make_float2(x[e][0], x[e][1]);
+      __syncthreads();
+      block_product<2>(x, sTb + r4, kTLd, sX + c, kTLd, 32);
+      const float4 b0 = *reinterpret_cast<const float4 *>(sTb + c * kTLd + r4);
+      const float4 b1 = *reinterpret_cast<const float4 *>(sTb + (c + 1) * kTLd + r4);
+      const float y0[4] = {b0.x, b0.y, b0.z, b0.w}, y1[4] = {b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = *reinterpret_cast<const float2 *>(sTa + (r4 + e) * kTLd + c);
+        put(r4 + e, c, v.x, v.y);
+        put(r4 + e, 32 + c, 0.f, 0.f);
+        put(32 + r4 + e, c, -x[e][0], -x[e][1]);
+        put(32 + r4 + e, 32 + c, y0[e], y1[e]);
+      }
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -109,7 +337,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
   uint32_t *tm_slot = reinterpret_cast<uint32_t *>(smem + kOffBar + kBars * 8 + 8);
   Scalars *scs = reinterpret_cast<Scalars *>(smem + kOffSc);
   const uint32_t base = smem_u32(smem);
-  constexpr int count[kBars] = {64, 64, 1, 1, 1, 1, 12, 12, 1, 1, 4, 4, 1, 1, 8, 8, 1, 1, 8, 1, 8, 8, 1, 4, 4, 1};
+  constexpr int count[kBars] = {64, 64, 1, 1, 1, 1, 4, 4, 1, 1, 8, 8, 1, 1, 8, 1, 8, 8, 1, 4, 2, 1};
   if (t == 0) {
     for (int i = 0; i < kBars; ++i) mbar_init(bar + i, count[i]);
     *abort = 0;
@@ -119,8 +347,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     umma::alloc(tm_slot, 512);
     umma::relinquish();
   }
-  for (int i = t; i < (kOffSc - kOffT) / 16; i += kThreadsG)   // T and M stay zero above the diagonal
-    reinterpret_cast<uint4 *>(smem + kOffT)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = t; i < (kOffSc - kOffM) / 16; i += kThreadsG)   // M stays zero above the diagonal
+    reinterpret_cast<uint4 *>(smem + kOffM)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
   umma::fence_before_sync();
   __syncthreads();
@@ -159,17 +387,27 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       warp_arrive(bar + kSp0 + half);
     };
     bool good = true;
-    if (chunks > 0) {
-#pragma unroll
-      for (int c = 0; c < 64; c += 16) {
-        put_state(c);
-        if (c & 16) state_ready(c >> 5);
-      }
-    }
-    for (int i = 0; i < chunks; ++i) {
+    float dec = 0.f;
+    for (int i = 0;; ++i) {
       const uint32_t ph = i & 1, sp = (i >> 1) & 1;
-      const Scalars &sc = scs[i & 1];
-      good = warp_wait(bar + kScFull0 + (i & 1), sp, abort, lim) && warp_wait(bar + kFull0 + (i & 1), sp, abort, lim);
+      const bool more = i < chunks;
+#pragma unroll
+      for (int c = 0; c < 64; c += 16) {   // the state before chunk i, and its parts
+        if (i > 0) {
+          float d[16];
+          umma::ld_32x32b_x16(lanes + kTmD + wg * 64 + c, d);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) S[c + j] = fmaf(dec, S[c + j], d[j]);
+        }
+        if (more) {
+          put_state(c);
+          if (c & 16) state_ready(c >> 5);
+        }
+      }
+      umma::fence_before_sync();
+      if (!more) break;
+      const Scalars &sc = scs[i & 3];
+      good = warp_wait(bar + kFull0 + (i & 1), sp, abort, lim);
       if (!good) break;
       float v[32];   // b v of this half's 32 tokens
       {
@@ -228,23 +466,10 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       wait_st();
       umma::fence_before_sync();
       warp_arrive(bar + kFwp);
-      const float dec = sc.last;
-      warp_arrive(bar + kScFree0 + (i & 1));
+      dec = sc.last;
       good = warp_wait(bar + kUpd, ph, abort, lim);
       if (!good) break;
       umma::fence_after_sync();
-      const bool more = i + 1 < chunks;
-#pragma unroll
-      for (int c = 0; c < 64; c += 16) {
-        float d[16];
-        umma::ld_32x32b_x16(lanes + kTmD + wg * 64 + c, d);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) S[c + j] = fmaf(dec, S[c + j], d[j]);
-        if (more) {
-          put_state(c);
-          if (c & 16) state_ready(c >> 5);
-        }
-      }
     }
     if (good) {
       float *dst = a.hc + (((size_t)q.dst * a.H + h) * kD + row) * kD + wg * 64;
@@ -253,43 +478,32 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     }
     }
   } else if (warp < 16) {
-    // ------------------------------- A, M, T and the outputs of every second chunk
-    fewer_registers<kRegsIntra>();
+    // ------------------------------------- M and the outputs of every second chunk
+    fewer_registers<kRegsOut>();
     const int me4 = (warp - 8) >> 2, w = warp & 3, r = w * 32 + lane;
-    const int sync_all = 1 + me4 * 3;   // named barriers of this warpgroup
     const uint32_t lanes = tm + ((uint32_t)(w * 32) << 16);
-    float *sA = reinterpret_cast<float *>(smem + kOffT + me4 * 3 * kPart);
-    float *sTa = reinterpret_cast<float *>(smem + kOffTa + me4 * kScratch);
-    float *sTb = reinterpret_cast<float *>(smem + kOffTb + me4 * kScratch);
-    float *sX = reinterpret_cast<float *>(smem + kOffX + me4 * kScratch);
     while (next()) {
     const int chunks = (q.n + kT - 1) / kT;
     for (int i = me4; i < chunks; i += 2) {
       const int buf = me4;
-      const Scalars &sc = scs[buf];
-      const bool ok = warp_wait(bar + kScFull0 + buf, (i >> 1) & 1, abort, lim) &&
-                      warp_wait(bar + kA0 + buf, (i >> 1) & 1, abort, lim) &&
-                      (i < 2 || warp_wait(bar + kStage0 + buf, ((i >> 1) - 1) & 1, abort, lim));   // T and M are read
-      if (named_sync_or(sync_all, 128, !ok)) break;   // the four warps agree; the chunk before's blocks are read
-      umma::fence_after_sync();
-      const int tt = r & 63;
-      const float2 me = sc.g[tt];
-      const float mul = w < 2 ? sc.be[tt] : a.out_scale;
-      const int top = w < 2 ? tt - 1 : tt;         // last column of this row
+      const Scalars &sc = scs[i & 3];
+      if (!warp_wait(bar + kFull0 + buf, (i >> 1) & 1, abort, lim)) break;
+      if (w >= 2) {   // a row of M per lane
+        if (!warp_wait(bar + kA0 + buf, (i >> 1) & 1, abort, lim) ||
+            (i > 1 && !warp_wait(bar + kStage0 + buf, ((i >> 1) - 1) & 1, abort, lim)))   // the last M is read
+          break;
+        umma::fence_after_sync();
+        const int tt = r - 64;
+        const float2 me = sc.g[tt];
+#pragma unroll 1
+        for (int cb = 0; cb < (w == 2 ? 2 : 4); ++cb) {     // up to the diagonal
+          float v[16];
+          umma::ld_32x32b_x16(lanes + kTmA + cb * 16, v);
 #pragma unroll
-      for (int cb = 0; cb < 4; ++cb) {
-        if (cb >= 2 && (w & 1) == 0) continue;     // above the diagonal
-        float v[16];
-        umma::ld_32x32b_x16(lanes + kTmA + cb * 16, v);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float2 o = sc.g[cb * 16 + j];
-          v[j] = cb * 16 + j <= top ? mul * (ex2((me.x - o.x) + (me.y - o.y)) * v[j]) : 0.f;
-        }
-        if (w < 2) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) sA[(cb * 16 + j) * kALd + tt] = v[j];
-        } else {
+          for (int j = 0; j < 16; ++j) {
+            const float2 o = sc.g[cb * 16 + j];
+            v[j] = cb * 16 + j <= tt ? a.out_scale * (ex2((me.x - o.x) + (me.y - o.y)) * v[j]) : 0.f;
+          }
 #pragma unroll
           for (int j = 0; j < 16; j += 8) {
             uint4 o[3];
@@ -301,102 +515,18 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
               *reinterpret_cast<uint4 *>(smem + kOffM + (buf * 3 + p) * kPart + sw128(tt, cb * 2 + j / 8)) = o[p];
           }
         }
+        umma::fence_before_sync();
+        fence_proxy_async();
+        warp_arrive(bar + kAfree);
       }
-      umma::fence_before_sync();
-      warp_arrive(bar + kAfree);
-      named_sync(sync_all, 128);
-      // T by blocks.  Sixteen-wide diagonal blocks by substitution, one per warp, a column per
-      // lane; then T_10 = -T_11 (A_10 T_00) for pairs of blocks, and again for pairs of those.
-      {
-        const int c = lane & 15;
-        float acc[16], val[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          val[k] = k == c ? 1.f : -acc[k];
-#pragma unroll
-          for (int j = (k + 1) / 4 * 4; j < 16; j += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(sA + (w * 16 + k) * kALd + w * 16 + j);
-            const float xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (j + e > k) acc[j + e] = fmaf(xs[e], val[k], acc[j + e]);
-          }
-        }
-        if (lane < 16) {
-          const int o = (w & 1) * 16;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            if (w < 2) sTa[(o + k) * kTLd + o + c] = val[k];
-            if (w == 1) sX[c * kXLd + k] = val[k];                    // T_11 by columns
-            if (w == 2) sX[(16 + k) * kXLd + c] = val[k];             // T_22 by rows
-          }
-          if (w >= 2) {
-#pragma unroll
-            for (int k = 0; k < 16; k += 4)
-              *reinterpret_cast<float4 *>(sTb + (o + c) * kTLd + o + k) = make_float4(val[k], val[k + 1], val[k + 2], val[k + 3]);
-          }
-        }
-      }
-      named_sync(sync_all, 128);
-      {
-        const int pr = w >> 1, id = r & 63, c = id & 15, r4 = (id >> 4) * 4;
-        float x[4][1];
-        float *sXp = sX + (32 + pr * 16) * kXLd;
-        block_product<1>(x, sA + (pr * 32) * kALd + pr * 32 + 16 + r4, kALd, pr ? sX + 16 * kXLd + c : sTa + c,
-                         pr ? kXLd : kTLd, 16);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sXp[(r4 + e) * kXLd + c] = x[e][0];
-        named_sync(sync_all + 1 + pr, 64);
-        block_product<1>(x, pr ? sTb + 16 * kTLd + 16 + r4 : sX + r4, pr ? kTLd : kXLd, sXp + c, kXLd, 16);
-        if (pr) {
-          *reinterpret_cast<float4 *>(sTb + c * kTLd + 16 + r4) = make_float4(-x[0][0], -x[1][0], -x[2][0], -x[3][0]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sTa[(16 + r4 + e) * kTLd + c] = -x[e][0];
-        }
-      }
-      named_sync(sync_all, 128);
-      {
-        const int c = (r & 15) * 2, r4 = (r >> 4) * 4;
-        auto put = [&](int row, int col, float v0, float v1) {
-          uint32_t hi, mid, lo;
-          split3(v0, v1, hi, mid, lo);
-          uint8_t *at = smem + kOffT + buf * 3 * kPart + sw128(row, col >> 3) + (col & 7) * 2;
-          *reinterpret_cast<uint32_t *>(at) = hi;
-          *reinterpret_cast<uint32_t *>(at + kPart) = mid;
-          *reinterpret_cast<uint32_t *>(at + 2 * kPart) = lo;
-        };
-        float x[4][2];
-        block_product<2>(x, sA + 32 + r4, kALd, sTa + c, kTLd, 32);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) *reinterpret_cast<float2 *>(sX + (r4 + e) * kTLd + c) = make_float2(x[e][0], x[e][1]);
-        named_sync(sync_all, 128);   // A is read: its place takes T's parts
-        block_product<2>(x, sTb + r4, kTLd, sX + c, kTLd, 32);
-        const float4 b0 = *reinterpret_cast<const float4 *>(sTb + c * kTLd + r4);
-        const float4 b1 = *reinterpret_cast<const float4 *>(sTb + (c + 1) * kTLd + r4);
-        const float y0[4] = {b0.x, b0.y, b0.z, b0.w}, y1[4] = {b1.x, b1.y, b1.z, b1.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 v = *reinterpret_cast<const float2 *>(sTa + (r4 + e) * kTLd + c);
-          put(r4 + e, c, v.x, v.y);
-          put(r4 + e, 32 + c, 0.f, 0.f);
-          put(32 + r4 + e, 32 + c, y0[e], y1[e]);
-        }
-
-#pragma unroll
-        for (int e = 0; e < 4; ++e) put(32 + r4 + e, c, -x[e][0], -x[e][1]);
-      }
-      fence_proxy_async();
-      warp_arrive(bar + kTm0 + buf);
-      // the chunk's outputs, a value row per lane (a give-up is agreed on at the loop's head)
-      if (!warp_wait(bar + kO0 + buf, (i >> 1) & 1, abort, lim)) continue;
+      warp_arrive(bar + kM0 + buf);   // of all four warps: none may miss a phase of kFull
+      // the chunk's outputs, a value row per lane
+      if (!warp_wait(bar + kO0 + buf, (i >> 1) & 1, abort, lim)) break;
       umma::fence_after_sync();
       const int left = q.n - i * kT;
       const size_t step = (size_t)a.H * kD;
       float *o = a.out + ((size_t)(q.tok + i * kT) * a.H + h) * kD + r;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < kT; c += 16) {
         float u[16], z[16];
         umma::ld_32x32b_x16(lanes + kTmU + c, u);
@@ -413,16 +543,10 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
           u[j + 2] = fmaf(g.z, z[j + 2], u[j + 2]);
           u[j + 3] = fmaf(g.w, z[j + 3], u[j + 3]);
         }
-        if (left >= kT) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j, o += step) __stcs(o, u[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j, o += step)
-            if (c + j < left) __stcs(o, u[j]);
-        }
+        for (int j = 0; j < 16; ++j, o += step)
+          if (c + j < left) __stcs(o, u[j]);
       }
-      warp_arrive(bar + kScFree0 + buf);
     }
     }
   } else if (warp == 16) {
@@ -443,7 +567,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     // S (rows of tile)^T over half of the columns: 32 from either half of the chain
     auto state_product = [&](uint32_t d, uint32_t tile, int half) {
       if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
         for (int p = 2; p >= 0; --p)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -460,7 +584,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     };
     auto pair_product = [&](uint32_t parts, uint32_t tile, uint64_t *b) {   // into U's place
       if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 6; ++c)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -492,20 +616,19 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
         umma::fence_after_sync();
         gram(i + 1);
       }
-      if (!warp_wait(bar + kTm0 + (i & 1), (i >> 1) & 1, abort, lim)) break;
       if (!warp_wait(bar + kRp, ph, abort, lim)) break;
       umma::fence_after_sync();
       pair_product(kTmR, base + kOffT + (i & 1) * 3 * kPart, bar + kW);
       state_product(kTmZ, kq + kPart, 0);   // while the chain splits W
       state_product(kTmZ, kq + kPart, 1);
       done(bar + kQ);
-      if (!warp_wait(bar + kWp, ph, abort, lim)) break;
+      if (!warp_wait(bar + kWp, ph, abort, lim) || !warp_wait(bar + kM0 + (i & 1), (i >> 1) & 1, abort, lim)) break;
       umma::fence_after_sync();
       pair_product(kTmW, base + kOffM + (i & 1) * 3 * kPart, bar + kO0 + (i & 1));
       if (!warp_wait(bar + kFwp, ph, abort, lim)) break;
       umma::fence_after_sync();
       if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
         for (int p = 2; p >= 0; --p)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -520,54 +643,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       warp_wait(bar + kStage0 + (i & 1), (i >> 1) & 1, abort, lim);
     }
   } else if (warp == 17) {
-    // -------------------------------------------------------- decays
     fewer_registers<kRegsRest>();
     while (next()) {
-    const int chunks = (q.n + kT - 1) / kT;
-    const float *pa = static_cast<const float *>(a.in[3]) + h, *pb = static_cast<const float *>(a.in[4]) + h;
-    auto load = [&](int i, float (&al)[2], float (&be)[2]) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int s = i * kT + lane * 2 + k;
-        const bool take = i < chunks && s < q.n;
-        al[k] = take ? pa[(int64_t)(q.tok + s) * a.stride[3]] : 1.f;
-        be[k] = take ? pb[(int64_t)(q.tok + s) * a.stride[4]] : 0.f;
-      }
-    };
-    float al[2], be[2];
-    load(0, al, be);
-    for (int i = 0; i < chunks; ++i) {
-      float aln[2], ben[2];
-      load(i + 1, aln, ben);
-      double g[2];
-      // a gate of 0 forgets all: any power of two this far down does
-      g[0] = fmax(log2((double)al[0]), -16384.0);
-      g[1] = g[0] + fmax(log2((double)al[1]), -16384.0);
-      double inc = g[1];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += up;
-      }
-      const double before = inc - g[1], last = __shfl_sync(0xffffffffu, inc, 31);
-      if (i > 1 && !warp_wait(bar + kScFree0 + (i & 1), ((i >> 1) - 1) & 1, abort, lim)) break;
-      Scalars &sc = scs[i & 1];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const double G = g[k] + before;
-        const float hi = (float)G;
-        sc.g[lane * 2 + k] = make_float2(hi, (float)(G - (double)hi));
-        const float e = ex2((float)G);
-        sc.be[lane * 2 + k] = be[k];
-        sc.bg[lane * 2 + k] = be[k] * e;
-        sc.zg[lane * 2 + k] = a.out_scale * e;
-        sc.fw[lane * 2 + k] = ex2((float)(last - G));
-        al[k] = aln[k];
-        be[k] = ben[k];
-      }
-      if (lane == 0) sc.last = ex2((float)last);
-      warp_arrive(bar + kScFull0 + (i & 1));
-    }
     }
   } else {
     // -------------------------------------------------------- tiles
@@ -582,6 +659,12 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       const int st = i & 1;
       if (i > 1 && !warp_wait(bar + kStage0 + st, ((i >> 1) - 1) & 1, abort, lim)) break;
       const uint32_t kq = base + kOffKQ + st * 2 * kBlk, v = base + kOffV + st * kBlk;
+      if (l == 0) {
+        const uint8_t *rec = a.parts + ((size_t)(q.first + i) * a.H + h) * kRecord;
+        mbar_expect_tx(bar + kFull0 + st, 3 * kPart + (uint32_t)sizeof(Scalars));
+        bulk_g2s(smem + kOffT + st * 3 * kPart, rec, 3 * kPart, bar + kFull0 + st);
+        bulk_g2s(scs + (i & 3), rec + 3 * kPart, sizeof(Scalars), bar + kFull0 + st);
+      }
       for (int j = l; j < kT * 16; j += 64) {
         const int s = j >> 4, c = j & 15;
         const bool take = i * kT + s < q.n;
@@ -623,10 +706,18 @@ bool gdn_chunk_path(const PrefillArgs &a, int in_dtype) {
   return a.kind == RSSM_GDN && in_dtype == RSSM_BF16 && a.R == kD && a.C == kD;
 }
 
+size_t gdn_chunk_work(int n_seq, int n_tokens, int H) {
+  return ((size_t)n_tokens / kT + n_seq) * H * kRecord;
+}
+
 cudaError_t gdn_chunk_prefill(const PrefillArgs &a, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemG);
+  cudaError_t e = cudaFuncSetAttribute(gdn_pre_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPre);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemG);
   if (e != cudaSuccess) return e;
-  const size_t items = (size_t)a.n_seq * a.H;
+  const size_t chunks = ((size_t)a.n_tokens / kT + a.n_seq) * a.H, items = (size_t)a.n_seq * a.H;
+  e = launch_early(gdn_pre_kernel, (unsigned)(chunks < 4 * kPrefillSms ? chunks : 4 * kPrefillSms), kPreThreads, kSmemPre,
+                   s, a);
+  if (e != cudaSuccess) return e;
   return launch_early(gdn_chunk_kernel, (unsigned)(items < kPrefillSms ? items : kPrefillSms), kThreadsG, kSmemG, s, a);
 }
 

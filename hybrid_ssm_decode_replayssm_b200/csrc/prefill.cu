@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
           place += m > full || (m == full && j < i);
         }
       }
-      PrefillSeq q;
+      PrefillSeq q = {};
       q.tok = o0;
       q.n = n;
       q.src = src;
@@ -87,6 +87,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
       if (n > a.scan_most) atomicMax(a.queue + kLongCount, place + 1);
     }
     rank += tot;
+  }
+  if (a.parts) {   // the long sequences' chunks, in the order of the list
+    __syncthreads();
+    int total = 0;
+    for (int i0 = 0; i0 < a.n_seq; i0 += nt) {
+      const int i = i0 + t;
+      const int n = i < a.n_seq ? a.seqs[i].n : 0;
+      int excl, tot;
+      block_scan(n > a.scan_most ? (n + 63) / 64 : 0, excl, tot);
+      if (i < a.n_seq) a.seqs[i].first = total + excl;
+      total += tot;
+    }
+    if (t == 0) a.queue[kChunkTotal] = total;
   }
 }
 
@@ -572,10 +585,15 @@ constexpr int kScanMost = 24;
 
 size_t seq_bytes(int n_seq) { return ((size_t)n_seq * sizeof(PrefillSeq) + 255) & ~(size_t)255; }
 
+size_t fixed_bytes(int n_seq, int batch) {
+  return (seq_bytes(n_seq) + (kCounters + kSmCounters + (size_t)batch) * sizeof(int32_t) + 255) & ~(size_t)255;
+}
+
 }  // namespace
 
 size_t prefill_work_bytes(const rssm_layer_desc &d, int n_seq, int n_tokens) {
-  return seq_bytes(n_seq) + (kCounters + kSmCounters + (size_t)d.batch) * sizeof(int32_t);
+  const bool parts = d.kind == RSSM_GDN && d.in_dtype == RSSM_BF16 && n_tokens > kScanMost;
+  return fixed_bytes(n_seq, d.batch) + (parts ? gdn_chunk_work(n_seq, n_tokens, d.nheads) : 0);
 }
 
 cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *launches, cudaStream_t s) {
@@ -586,13 +604,14 @@ cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *
   const bool m2_chunks = m2_chunk_path(a, in_dtype), gdn_chunks = gdn_chunk_path(a, in_dtype);
   const bool chunks = (m2_chunks || gdn_chunks) && a.n_tokens > kScanMost;
   a.scan_most = chunks ? kScanMost : a.n_tokens;
+  a.parts = chunks && gdn_chunks ? static_cast<uint8_t *>(work) + fixed_bytes(a.n_seq, a.B) : nullptr;
   plan_prefill_kernel<<<1, kPlanThreads, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   ++*launches;
   if (e != cudaSuccess) return e;
   if (chunks) {
     e = m2_chunks ? m2_chunk_prefill(a, s) : gdn_chunk_prefill(a, s);
-    ++*launches;
+    *launches += m2_chunks ? 1 : 2;
     if (e != cudaSuccess) return e;
   }
   const bool bf16 = in_dtype == RSSM_BF16;

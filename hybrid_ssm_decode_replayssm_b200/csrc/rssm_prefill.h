@@ -9,13 +9,15 @@ namespace rssm {
 // One sequence of a prefill call as its planner decided it: tokens
 // [tok, tok + n) of the packed inputs, the checkpoint slots it reads (src, -1 =
 // zero state) and writes (dst).  dst = -1: refused, or nothing to do.
+// first: its first chunk in the list of the long sequences' chunks.
 struct PrefillSeq {
-  int32_t tok, n, src, dst;
+  int32_t tok, n, src, dst, first, pad[3];
 };
 
 // Counters in the workspace: three of the token scan's items, one of the chunked
-// kernels', the number of sequences up to the last long one; then CTAs begun per SM.
-enum { kScanTaken = 0, kScanFront, kScanBack, kChunkQueue, kLongCount, kCounters };
+// kernels', the number of sequences up to the last long one, the long ones' chunks of 64
+// tokens; then CTAs begun per SM.
+enum { kScanTaken = 0, kScanFront, kScanBack, kChunkQueue, kLongCount, kChunkTotal, kCounters };
 constexpr int kSmCounters = 256 - kCounters;
 constexpr int kPrefillSms = 148;   // CTAs of the persistent kernels, one per SM
 
@@ -34,6 +36,7 @@ struct PrefillArgs {
   // workspace: the planned sequences, longest first, work counters, and a counter per row
   PrefillSeq *seqs;
   int32_t *queue;
+  uint8_t *parts;             // GDN: T of every long sequence's chunks and heads, in three bf16 parts
   int32_t *named;
   // bookkeeping
   int32_t *len, *pending, *flushes;
@@ -56,7 +59,8 @@ cudaError_t m2_chunk_prefill(const PrefillArgs &a, cudaStream_t s);   // sequenc
 
 // The chunked gated delta rule (gdn_prefill.cu): GDN, bf16 inputs.
 bool gdn_chunk_path(const PrefillArgs &a, int in_dtype);
-cudaError_t gdn_chunk_prefill(const PrefillArgs &a, cudaStream_t s);
+size_t gdn_chunk_work(int n_seq, int n_tokens, int H);
+cudaError_t gdn_chunk_prefill(const PrefillArgs &a, cudaStream_t s);   // two kernels
 
 // Launch with programmatic stream serialisation: the kernel may begin before the grid
 // ahead of it ends, and waits for it itself.
