@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     // S (rows of tile)^T over half of the columns: 32 from either half of the chain
     auto state_product = [&](uint32_t d, uint32_t tile, int half) {
       if (elect_one()) {
-#pragma unroll 1
+#pragma unroll
         for (int p = 2; p >= 0; --p)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     };
     auto pair_product = [&](uint32_t parts, uint32_t tile, uint64_t *b) {   // into U's place
       if (elect_one()) {
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < 6; ++c)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -610,25 +610,25 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       umma::fence_after_sync();
       state_product(kTmU, kq, 1);
       done(bar + kU);
-      if (i + 1 < chunks) {   // while the chain makes R
+      state_product(kTmZ, kq + kPart, 0);   // while the chain makes R
+      state_product(kTmZ, kq + kPart, 1);
+      done(bar + kQ);
+      if (!warp_wait(bar + kRp, ph, abort, lim)) break;
+      umma::fence_after_sync();
+      pair_product(kTmR, base + kOffT + (i & 1) * 3 * kPart, bar + kW);
+      if (i + 1 < chunks) {   // while the chain splits W
         if (!warp_wait(bar + kAfree, ph, abort, lim)) break;
         if (!warp_wait(bar + kFull0 + ((i + 1) & 1), ((i + 1) >> 1) & 1, abort, lim)) break;
         umma::fence_after_sync();
         gram(i + 1);
       }
-      if (!warp_wait(bar + kRp, ph, abort, lim)) break;
-      umma::fence_after_sync();
-      pair_product(kTmR, base + kOffT + (i & 1) * 3 * kPart, bar + kW);
-      state_product(kTmZ, kq + kPart, 0);   // while the chain splits W
-      state_product(kTmZ, kq + kPart, 1);
-      done(bar + kQ);
       if (!warp_wait(bar + kWp, ph, abort, lim) || !warp_wait(bar + kM0 + (i & 1), (i >> 1) & 1, abort, lim)) break;
       umma::fence_after_sync();
       pair_product(kTmW, base + kOffM + (i & 1) * 3 * kPart, bar + kO0 + (i & 1));
       if (!warp_wait(bar + kFwp, ph, abort, lim)) break;
       umma::fence_after_sync();
       if (elect_one()) {
-#pragma unroll 1
+#pragma unroll
         for (int p = 2; p >= 0; --p)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
