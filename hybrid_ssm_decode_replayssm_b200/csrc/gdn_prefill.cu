@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
   constexpr int count[kBars] = {64, 64, 1, 1, 1, 1, 4, 4, 1, 1, 8, 8, 1, 1, 8, 1, 8, 8, 1, 4, 2, 1};
   if (t == 0) {
     for (int i = 0; i < kBars; ++i) mbar_init(bar + i, count[i]);
-    *abort = 0;
+    abort[0] = abort[1] = 0;   // the second is never set
     mbar_fence_init();
   }
   if (warp == 16) {
@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     };
     bool good = true;
     float dec = 0.f;
+    if (a.stall_test && blockIdx.x == 0) stall_on_unset_flag(const_cast<int *>(abort) + 1, abort, lim);
     for (int i = 0;; ++i) {
       const uint32_t ph = i & 1, sp = (i >> 1) & 1;
       const bool more = i < chunks;
@@ -655,6 +656,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     const __nv_bfloat16 *in[3];
 #pragma unroll
     for (int k = 0; k < 3; ++k) in[k] = static_cast<const __nv_bfloat16 *>(a.in[k]) + (size_t)h * kD;
+    int issued = 0;
     for (int i = 0; i < chunks; ++i) {
       const int st = i & 1;
       if (i > 1 && !warp_wait(bar + kStage0 + st, ((i >> 1) - 1) & 1, abort, lim)) break;
@@ -678,8 +680,12 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       cp_wait<0>();
       fence_proxy_async();
       mbar_arrive(bar + kFull0 + st);
+      issued = i + 1;
     }
     cp_async_wait_all();
+    // the bulk copies have landed before this CTA goes on, or ends, whatever came
+    for (int i = issued > 1 ? issued - 2 : 0; i < issued; ++i)
+      mbar_wait_bounded(bar + kFull0 + (i & 1), (i >> 1) & 1, nullptr, lim);
     }
   }
   // -------------------------------------------------------- end
@@ -711,8 +717,8 @@ size_t gdn_chunk_work(int n_seq, int n_tokens, int H) {
 }
 
 cudaError_t gdn_chunk_prefill(const PrefillArgs &a, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(gdn_pre_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPre);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(gdn_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemG);
+  cudaError_t e = allow_smem(gdn_pre_kernel, kSmemPre);
+  if (e == cudaSuccess) e = allow_smem(gdn_chunk_kernel, kSmemG);
   if (e != cudaSuccess) return e;
   const size_t chunks = ((size_t)a.n_tokens / kT + a.n_seq) * a.H, items = (size_t)a.n_seq * a.H;
   e = launch_early(gdn_pre_kernel, (unsigned)(chunks < 4 * kPrefillSms ? chunks : 4 * kPrefillSms), kPreThreads, kSmemPre,

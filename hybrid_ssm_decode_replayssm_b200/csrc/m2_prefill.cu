@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
   constexpr int count[kBars] = {128, 128, 8, 1, 1, 8, 1, 1, 8, 8, 8, 8, 8, 8, 1, 16, 8, 8, 1};
   if (t == 0) {
     for (int i = 0; i < kBars; ++i) mbar_init(bar + i, count[i]);
-    *abort = 0;
+    abort[0] = abort[1] = 0;   // the second is never set
     mbar_fence_init();
   }
   if (warp == 16) {
@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       warp_arrive(bar + kHp);
     };
     bool good = true;
+    if (a.stall_test && blockIdx.x == 0) stall_on_unset_flag(const_cast<int *>(abort) + 1, abort, lim);
     if (chunks > 0) {
       put_state(0);
       put_state(16);
@@ -465,7 +466,7 @@ bool m2_chunk_path(const PrefillArgs &a, int in_dtype) {
 
 cudaError_t m2_chunk_prefill(const PrefillArgs &a, cudaStream_t s) {
   auto kernel = a.C == 64 ? m2_chunk_kernel<64> : m2_chunk_kernel<128>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemM);
+  const cudaError_t e = allow_smem(kernel, kSmemM);
   if (e != cudaSuccess) return e;
   const size_t items = (size_t)a.n_seq * a.H;
   return launch_early(kernel, (unsigned)(items < kPrefillSms ? items : kPrefillSms), kThreadsM, kSmemM, s, a);

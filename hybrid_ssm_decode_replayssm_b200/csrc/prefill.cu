@@ -59,8 +59,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
         a.flushes[r] += 1;
       }
     }
-    int excl, tot;
-    block_scan(take, excl, tot);
+    int excl = 0, tot = 0;
+    if (a.slot) block_scan(take, excl, tot);
     if (i < a.n_seq) {
       int to = -1;
       if (take) {
@@ -580,8 +580,13 @@ cudaError_t launch_scan(const PrefillArgs &a, bool behind_chunks, cudaStream_t s
 }
 
 // Sequences of up to this many tokens run four tokens at a time even where a chunked kernel
-// serves the layer, whose first chunk costs as much as a full one.
-constexpr int kScanMost = 24;
+// serves the layer, whose first chunk costs as much as a full one (32 sequences on 32 GDN
+// heads: at 32 tokens 117 us against 147, at 64 tokens 217 against 163; Mamba-2 on 128
+// heads 180 against 240 and 309 against 246).  A GDN call of few tokens in all does without
+// the chunked kernels' two launches (192 tokens in one sequence: 38 us either way).
+constexpr int kScanMost = 40, kGdnFew = 192;
+
+bool chunked(int kind, int n_tokens) { return n_tokens > (kind == RSSM_GDN ? kGdnFew : kScanMost); }
 
 size_t seq_bytes(int n_seq) { return ((size_t)n_seq * sizeof(PrefillSeq) + 255) & ~(size_t)255; }
 
@@ -592,7 +597,7 @@ size_t fixed_bytes(int n_seq, int batch) {
 }  // namespace
 
 size_t prefill_work_bytes(const rssm_layer_desc &d, int n_seq, int n_tokens) {
-  const bool parts = d.kind == RSSM_GDN && d.in_dtype == RSSM_BF16 && n_tokens > kScanMost;
+  const bool parts = d.kind == RSSM_GDN && d.in_dtype == RSSM_BF16 && chunked(d.kind, n_tokens);
   return fixed_bytes(n_seq, d.batch) + (parts ? gdn_chunk_work(n_seq, n_tokens, d.nheads) : 0);
 }
 
@@ -602,7 +607,7 @@ cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *
   a.named = a.queue + kCounters + kSmCounters;
   *launches = 0;
   const bool m2_chunks = m2_chunk_path(a, in_dtype), gdn_chunks = gdn_chunk_path(a, in_dtype);
-  const bool chunks = (m2_chunks || gdn_chunks) && a.n_tokens > kScanMost;
+  const bool chunks = (m2_chunks || gdn_chunks) && chunked(a.kind, a.n_tokens);
   a.scan_most = chunks ? kScanMost : a.n_tokens;
   a.parts = chunks && gdn_chunks ? static_cast<uint8_t *>(work) + fixed_bytes(a.n_seq, a.B) : nullptr;
   plan_prefill_kernel<<<1, kPlanThreads, 0, s>>>(a);

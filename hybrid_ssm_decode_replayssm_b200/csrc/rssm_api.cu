@@ -629,6 +629,8 @@ int rssm_prefill(rssm_handle *h, int n_seq, int n_tokens, const int32_t *offsets
   }
   a.rc_codes = p.rc_codes; a.rc_scales = p.rc_scales;
   a.wait_limit = h->wait_limit;
+  a.stall_test = h->stall_next;
+  h->stall_next = 0;
   int launches = 0;
   const cudaError_t e = rssm::prefill(a, work_dev, d.in_dtype, d.read_fmt, &launches, (cudaStream_t)stream);
   g_launches.fetch_add(launches, std::memory_order_relaxed);

@@ -2,6 +2,8 @@
 // the C-ABI host code.
 #pragma once
 
+#include <atomic>
+
 #include "rssm_internal.h"
 
 namespace rssm {
@@ -46,6 +48,7 @@ struct PrefillArgs {
   uint8_t *rc_codes;
   void *rc_scales;
   long long wait_limit;
+  int stall_test;             // the first CTA of a chunked kernel takes the timeout path
 };
 
 // Bytes of the caller's workspace of one call.
@@ -61,6 +64,28 @@ cudaError_t m2_chunk_prefill(const PrefillArgs &a, cudaStream_t s);   // sequenc
 bool gdn_chunk_path(const PrefillArgs &a, int in_dtype);
 size_t gdn_chunk_work(int n_seq, int n_tokens, int H);
 cudaError_t gdn_chunk_prefill(const PrefillArgs &a, cudaStream_t s);   // two kernels
+
+// Dynamic shared memory beyond the default, asked for once per kernel and device.
+inline cudaError_t allow_smem(void (*kernel)(PrefillArgs), int bytes) {
+  struct Seen {
+    std::atomic<void (*)(PrefillArgs)> kernel[8];
+    std::atomic<int> n;
+  };
+  static Seen seen[64];   // by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  Seen *s = dev >= 0 && dev < 64 ? &seen[dev] : nullptr;
+  if (s)
+    for (int i = 0, n = s->n.load(std::memory_order_acquire); i < n && i < 8; ++i)
+      if (s->kernel[i].load(std::memory_order_acquire) == kernel) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && s) {
+    const int i = s->n.fetch_add(1, std::memory_order_acq_rel);
+    if (i < 8) s->kernel[i].store(kernel, std::memory_order_release);
+  }
+  return e;
+}
 
 // Launch with programmatic stream serialisation: the kernel may begin before the grid
 // ahead of it ends, and waits for it itself.

@@ -227,7 +227,9 @@ int rssm_set_wait_limit(rssm_handle *h, long long cycles);
  * 128) run a kernel without waits: such a launch just clears the armed test.
  * KDA: only the decode serving kernel (bf16 inputs) waits, so only a decode of
  * such a handle takes the path (a verify or flush launch just clears the armed
- * test); a KDA handle with fp32 inputs gives RSSM_ERR_UNSUPPORTED. */
+ * test); a KDA handle with fp32 inputs gives RSSM_ERR_UNSUPPORTED.
+ * rssm_prefill takes the armed test too: its chunked kernels (Mamba-2 and GDN with
+ * bf16 inputs, long sequences) run the path, a call without them just clears it. */
 int rssm_arm_timeout_test(rssm_handle *h);
 
 /*

@@ -230,3 +230,62 @@ def test_the_same_call_twice_gives_the_same_bits():
             L.layer.prefill(toks, i32([0, 100, 101, 400, 650, 700]), out)
             res.append((out, L.layer.ckpt))
         assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_items_of_all_lengths(kind):
+    """More (sequence, head) items than SMs, short and long sequences, empty and refused ones in
+    one call: the persistent kernels take several items each."""
+    heads = 16
+    lens = [70, 1, 0, 300, 41, 40, 129, 64, 65, 25, 24, 256, 3, 128, 0, 90]
+    n = len(lens)
+    L = Layer(kind, batch=n + 3, heads=heads, groups=2 if kind == "mamba2" else 1)
+    rows = list(range(n))[::-1]
+    fresh = [i % 3 == 0 for i in range(n)]
+    toks = L.tokens(sum(lens), 17)
+    off = offsets_of(lens)
+    out = torch.full((off[-1], heads, L.R), -77.0, device=DEV)
+    rows[3] = rows[9] = n + 1                              # a long and a short one name one row
+    L.layer.prefill([t.to(DEV) for t in toks], i32(off), out, rows=i32(rows), fresh=i32([int(f) for f in fresh]))
+    assert L.layer.get_status(clear=True) == rssm.RSSM_STATUS_STATE
+    got, after = to64(out), L.rows()
+    for i, r in enumerate(rows):
+        o = got[off[i]:off[i + 1]]
+        if i in (3, 9):
+            assert (o == -77).all()
+            continue
+        S, want = L.ref_run(L.state[r] * (not fresh[i]), [t[off[i]:off[i + 1]] for t in toks])
+        assert max(scaled(o, want), scaled(after[r], S)) <= TOL, (i, lens[i])
+    for r in (n, n + 1, n + 2):
+        assert (after[r] == L.state[r]).all()
+
+
+@pytest.mark.parametrize("kind", ["gdn", "mamba2"])
+def test_outputs_of_one_sequence_do_not_depend_on_the_others(kind):
+    """A long sequence alone and in a batch gives the same bits (a short call may go by another
+    kernel, so the sequence is long enough for either)."""
+    L, M = (Layer(kind, batch=4, heads=4) for _ in range(2))
+    toks = [t.to(DEV) for t in L.tokens(700, 3)]
+    one = torch.zeros((400, 4, L.R), device=DEV)
+    L.layer.prefill([t[100:500].contiguous() for t in toks], i32([0, 400]), one, rows=i32([2]))
+    all_ = torch.zeros((700, 4, L.R), device=DEV)
+    M.layer.prefill(toks, i32([0, 100, 500, 510, 700]), all_, rows=i32([0, 2, 1, 3]))
+    assert torch.equal(one, all_[100:500]) and torch.equal(L.layer.ckpt[2], M.layer.ckpt[2])
+
+
+@pytest.mark.parametrize("kind", ["gdn", "mamba2"])
+def test_a_wait_that_runs_out_ends_the_call(kind):
+    """The armed self-test: a chunked kernel's wait gives up, the status says TIMEOUT, and after a
+    reset the layer works again."""
+    L = Layer(kind, batch=2, heads=80)                     # more items than SMs
+    toks = [t.to(DEV) for t in L.tokens(600, 3)]
+    out = torch.zeros((600, 80, L.R), device=DEV)
+    lib = rssm.lib()
+    rssm.check(lib.rssm_set_wait_limit(L.layer.handle, 2_000_000))     # about a millisecond
+    rssm.check(lib.rssm_arm_timeout_test(L.layer.handle))
+    L.layer.prefill(toks, i32([0, 300, 600]), out)
+    assert L.layer.get_status(clear=True) & rssm.RSSM_STATUS_TIMEOUT
+    rssm.check(lib.rssm_set_wait_limit(L.layer.handle, 0))
+    L.layer.reset()
+    L.layer.ckpt.copy_(L.h0.to(DEV))
+    run(L, [150, 70], [0, 1], [0, 0])
