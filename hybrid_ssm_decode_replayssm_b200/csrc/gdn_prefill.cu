@@ -153,10 +153,11 @@ __global__ void __launch_bounds__(kPreThreads, 4) gdn_pre_kernel(const PrefillAr
   float *sTb = reinterpret_cast<float *>(smem + kPreOffTb), *sX = reinterpret_cast<float *>(smem + kPreOffX);
   float2 *sG = reinterpret_cast<float2 *>(smem + kPreOffG);
   float *sBe = reinterpret_cast<float *>(smem + kPreOffG + kT * 8);
-  for (int i = t; i < (kPreOffG - kPreOffTa) / 4; i += kPreThreads) sTa[i] = 0.f;   // zero above the diagonal
   grid_wait();
   grid_launch_next();
   const int total = a.queue[kChunkTotal], longs = a.queue[kLongCount];
+  if (longs == 0) return;
+  for (int i = t; i < (kPreOffG - kPreOffTa) / 4; i += kPreThreads) sTa[i] = 0.f;   // zero above the diagonal
   for (size_t id = blockIdx.x; id < (size_t)total * a.H; id += gridDim.x) {
     const int h = (int)(id % a.H), chunk = (int)(id / a.H);
     int lo = 0, hi = longs - 1;   // the last sequence that begins at or before this chunk (and is not empty)
@@ -330,6 +331,9 @@ __global__ void __launch_bounds__(kPreThreads, 4) gdn_pre_kernel(const PrefillAr
 }
 
 __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillArgs a) {
+  grid_wait();
+  grid_launch_next();
+  if (a.queue[kLongCount] == 0) return;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kOffBar);
@@ -355,8 +359,6 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
   umma::fence_after_sync();
   const uint32_t tm = *tm_slot;
   const long long lim = a.wait_limit;
-  grid_wait();
-  grid_launch_next();
   PrefillSeq q;
   int h, *s_item = reinterpret_cast<int *>(smem + kOffBar + kBars * 8 + 12);
   auto next = [&]() { return next_item<kThreadsG, kBars>(a, bar, count, s_item, abort, q, h); };

@@ -57,6 +57,9 @@ constexpr int kTmCb = 0, kTmY = 128, kTmC = 192, kTmU = 256, kTmL = 320;
 
 template <int N>
 __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArgs a) {
+  grid_wait();
+  grid_launch_next();
+  if (a.queue[kLongCount] == 0) return;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kOffBar);
@@ -89,8 +92,6 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
   umma::fence_after_sync();
   const uint32_t tm = *tm_slot;
   const long long lim = a.wait_limit;
-  grid_wait();
-  grid_launch_next();
   PrefillSeq q;
   int h, *s_item = reinterpret_cast<int *>(smem + kOffBar + kBars * 8 + 12);
   auto next = [&]() { return next_item<kThreadsM, kBars>(a, bar, count, s_item, abort, q, h); };
