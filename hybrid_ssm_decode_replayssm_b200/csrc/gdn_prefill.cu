@@ -669,14 +669,23 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
         bulk_g2s(smem + kOffT + st * 3 * kPart, rec, 3 * kPart, bar + kFull0 + st);
         bulk_g2s(scs + (i & 3), rec + 3 * kPart, sizeof(Scalars), bar + kFull0 + st);
       }
-      for (int j = l; j < kT * 16; j += 64) {
-        const int s = j >> 4, c = j & 15;
-        const bool take = i * kT + s < q.n;
-        const int64_t tok = take ? q.tok + i * kT + s : q.tok;
-        const uint32_t to = kq + (c >> 3) * kBlk;
-        cp_async16_zfill(to + sw128(s, c & 7), in[1] + tok * a.stride[1] + c * 8, take);
-        cp_async16_zfill(to + sw128(64 + s, c & 7), in[0] + tok * a.stride[0] + c * 8, take);
-        cp_async16_zfill(v + s * 256 + c * 16, in[2] + tok * a.stride[2] + c * 8, take);
+      // a thread keeps its 16-byte column and takes every fourth row; the swizzle of the rows
+      // changes between two patterns
+      const int s0 = l >> 4, c = l & 15, left = q.n - i * kT - s0;
+      const int64_t first = q.tok + i * kT + s0;
+      const __nv_bfloat16 *at[3];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) at[k] = in[k] + first * a.stride[k] + c * 8;
+      const uint32_t to = kq + (c >> 3) * kBlk, even = to + sw128(s0, c & 7), odd = to + sw128(s0 + 4, c & 7);
+#pragma unroll
+      for (int k = 0; k < kT / 4; ++k) {
+        const bool take = left > k * 4;
+        const uint32_t row = (k & 1 ? odd : even) + (k >> 1) * 1024;
+        cp_async16_zfill(row, take ? at[1] : in[1], take);
+        cp_async16_zfill(row + 64 * 128, take ? at[0] : in[0], take);
+        cp_async16_zfill(v + (s0 + k * 4) * 256 + c * 16, take ? at[2] : in[2], take);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) at[j] += 4 * a.stride[j];
       }
       cp_commit();
       cp_wait<0>();

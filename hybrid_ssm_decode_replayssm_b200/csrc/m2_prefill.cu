@@ -55,6 +55,10 @@ static_assert(kSmemM <= 232448, "shared memory of one CTA");
 // tensor memory columns (kTmC: C as an operand)
 constexpr int kTmCb = 0, kTmY = 128, kTmC = 192, kTmU = 256, kTmL = 320;
 
+template <int N> struct Cols {
+  static constexpr int value = N;
+};
+
 template <int N>
 __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArgs a) {
   grid_wait();
@@ -111,14 +115,21 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
     const float Dh = __ldg(a.D + h);
     for (int i = 0; i < chunks; ++i) {
       const uint32_t ph = i & 1;
-      if (!warp_wait(bar + kScFull, ph, abort, lim) || !warp_wait(bar + kCb, ph, abort, lim)) break;
-      umma::fence_after_sync();
+      if (!warp_wait(bar + kScFull, ph, abort, lim)) break;
       const float4 me = sc[row];
       // below the diagonal blocks e^{G_t - G_s} splits at the block's start, and one
-      // factor per column is left
+      // factor per column is left; the diagonal block's are made while C B^T is
       const float4 ref = sc[w > 0 ? w * 32 - 1 : 0];
       const float at = ex2((me.x - ref.x) + (me.y - ref.y));
       const float *od = reinterpret_cast<const float *>(smem + kOffOd) + (w == 3 ? 96 : w == 2 ? 32 : 0);
+      float e[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float4 s = sc[w * 32 + wg * 16 + j];
+        e[j] = wg * 16 + j <= lane ? ex2((me.x - s.x) + (me.y - s.y)) * s.z : 0.f;
+      }
+      if (!warp_wait(bar + kCb, ph, abort, lim)) break;
+      umma::fence_after_sync();
       bool ok = true;
       for (int cb = 0; cb < 4; ++cb) {
         if (cb <= w) {
@@ -133,10 +144,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float4 s = sc[c0 + j];
-              v[j] = wg * 16 + j <= lane ? ex2((me.x - s.x) + (me.y - s.y)) * (s.z * v[j]) : 0.f;
-            }
+            for (int j = 0; j < 16; ++j) v[j] = wg * 16 + j <= lane ? e[j] * v[j] : 0.f;
           }
           split_store(lanes + kTmL + cb * 16 + wg * 8, 64, v);
         }
@@ -417,22 +425,27 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
     const __nv_bfloat16 *px = static_cast<const __nv_bfloat16 *>(a.in[0]) + (size_t)h * kP;
     const __nv_bfloat16 *pB = static_cast<const __nv_bfloat16 *>(a.in[1]) + (size_t)g * N;
     const __nv_bfloat16 *pC = static_cast<const __nv_bfloat16 *>(a.in[2]) + (size_t)g * N;
-    auto tile = [&](uint32_t to, const __nv_bfloat16 *p, int64_t stride, int i, int cols) {
-      const int per = cols / 8;
-      for (int j = l; j < kT * per; j += 128) {
-        const int s = j / per, c = j % per;
-        const bool take = i * kT + s < q.n;
-        const int tok = take ? q.tok + i * kT + s : q.tok;
-        cp_async16_zfill(to + (c / 8) * kBlk + sw128(s, c % 8), p + tok * stride + c * 8, take);
+    // a thread keeps its 16-byte column and takes every eighth (or sixteenth) row: the
+    // swizzle of its rows is the same
+    auto tile = [&](uint32_t to, const __nv_bfloat16 *p, int64_t stride, int i, auto cols) {
+      constexpr int per = decltype(cols)::value / 8, rows = 128 / per;
+      const int s0 = l / per, c = l % per, left = q.n - i * kT - s0;
+      const __nv_bfloat16 *at = p + (int64_t)(q.tok + i * kT + s0) * stride + c * 8;
+      uint32_t dst = to + (c / 8) * kBlk + sw128(s0, c % 8);
+#pragma unroll
+      for (int k = 0; k < kT / rows; ++k) {
+        cp_async16_zfill(dst, left > k * rows ? at : p, left > k * rows);
+        at += rows * stride;
+        dst += rows * 128;
       }
     };
     for (int i = 0; i < chunks; ++i) {
       const int st = i & 1;
       if (i > 1 && !warp_wait(bar + kStage0 + st, ((i >> 1) - 1) & 1, abort, lim)) break;
-      tile(base + kOffB + st * 2 * kBlk, pB, a.stride[1], i, N);
-      tile(base + kOffX + st * kBlk, px, a.stride[0], i, kP);
+      tile(base + kOffB + st * 2 * kBlk, pB, a.stride[1], i, Cols<N>());
+      tile(base + kOffX + st * kBlk, px, a.stride[0], i, Cols<kP>());
       if (i > 0 && !warp_wait(bar + kCt, (i - 1) & 1, abort, lim)) break;
-      tile(base + kOffC, pC, a.stride[2], i, N);
+      tile(base + kOffC, pC, a.stride[2], i, Cols<N>());
       cp_commit();
       cp_wait<0>();
       fence_proxy_async();
