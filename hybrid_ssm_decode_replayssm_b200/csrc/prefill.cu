@@ -20,6 +20,10 @@ namespace {
 // Accepted sequences are listed longest first, so that the longest start first.
 constexpr int kPlanThreads = 1024;
 
+constexpr int kFineTokens = 512;   // of a sequence, above which the token scan takes it by 32 rows
+constexpr int kBins = 66;
+__device__ __forceinline__ int length_bin(int n, int scan_most) { return (n > scan_most ? 33 : 0) + 32 - __clz(n); }
+
 __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const PrefillArgs a) {
   const int nt = blockDim.x, t = threadIdx.x;
   chunk::grid_launch_next();   // the kernels behind wait for this grid themselves
@@ -38,6 +42,26 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
   }
   int nfree = 0;
   if (a.slot) nfree = free_slots(a.B, a.slot, a.freelist);
+  // Up to 1024 sequences are sorted by comparing all pairs; more of them by powers of two of
+  // their lengths, those of the chunked kernels first (the order decides when a sequence
+  // runs, nothing in it).
+  const bool many = a.n_seq > kPlanThreads;
+  __shared__ int bins[kBins];
+  if (many) {
+    if (t < kBins) bins[t] = 0;
+    __syncthreads();
+    for (int i = t; i < a.n_seq; i += nt) {
+      const int n = bad ? 0 : a.offsets[i + 1] - a.offsets[i];
+      atomicAdd(bins + length_bin(n, a.scan_most), 1);
+    }
+    __syncthreads();
+    if (t == 0)
+      for (int b = kBins - 1, sum = 0; b >= 0; --b) {
+        const int c = bins[b];
+        bins[b] = sum;
+        sum += c;
+      }
+  }
   __syncthreads();
   int rank = 0;
   for (int i0 = 0; i0 < a.n_seq; i0 += nt) {
@@ -67,12 +91,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
         to = r;
         if (a.slot) a.dst[r] = to = rank + excl < nfree ? a.freelist[rank + excl] : a.slot[r];   // nfree >= B
       }
-      // the place of i: how many sequences are longer, or as long and before it
-      int place = 0;
-      if (bad) {
+      int place;
+      if (many) {
+        place = atomicAdd(bins + length_bin(bad ? 0 : a.offsets[i + 1] - a.offsets[i], a.scan_most), 1);
+      } else if (bad) {
         place = i;
-      } else {
+      } else {   // how many sequences are longer, or as long and before it
         const int full = a.offsets[i + 1] - a.offsets[i];
+        place = 0;
         for (int j = 0; j < a.n_seq; ++j) {
           const int m = a.offsets[j + 1] - a.offsets[j];
           place += m > full || (m == full && j < i);
@@ -85,6 +111,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
       q.dst = to;
       a.seqs[place] = q;
       if (n > a.scan_most) atomicMax(a.queue + kLongCount, place + 1);
+      else if (n > kFineTokens) atomicMax(a.queue + kFineCount, place + 1);
     }
     rank += tot;
   }
@@ -171,30 +198,32 @@ struct __align__(16) ScanBlock {
   float pc, pad[3];
 };
 
-template <int KIND, typename Tin, int C, int ROWS>
-__global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs a, int items, bool behind_chunks) {
+template <int N> struct Const {
+  static constexpr int value = N;
+};
+
+template <int KIND, typename Tin, int C>
+__global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs a, int fine_all, bool behind_chunks) {
   constexpr bool M2 = KIND == RSSM_MAMBA2, KDA = KIND == RSSM_KDA;
   constexpr int LPR = C / 16;                       // lanes per row
   constexpr int GROUPS = 128 / LPR;                 // rows per pass: 16 or 32
-  constexpr int RPT = ROWS / GROUPS;                // rows per thread
-  constexpr int NV = RPT * 4;                       // a thread's sums for four tokens
-  constexpr int PL = NV / LPR, LR = 4 / PL;         // the sums it keeps; lanes that hold a row's four
-  static_assert(PL == 1 || PL == 2, "sums per lane");
   struct Buf {
     float k[kScanTok][C], q[kScanTok][C];           // KDA: p_i k_i, p_i q_i
     float kt[KDA ? kScanTok : 1][C], pc[KDA ? 2 : 1][C];   // KDA: d_3j k_j, p_3
-    float v[kScanTok][ROWS], o[kScanTok][ROWS];
+    float v[kScanTok][64], o[kScanTok][64];
     ScanBlock blk[2];
   };
   __shared__ __align__(16) Buf buf[2];
   __shared__ __align__(16) float raw_k[KDA ? kScanTok : 1][C], raw_g[KDA ? kScanTok : 1][C];
   __shared__ __align__(16) float s_gate[kScanTok], s_beta[kScanTok];
   __shared__ int s_item;
-  const int slices = a.R / ROWS;
   // alone, this grid waits for the planner's; behind a chunked kernel, whose CTAs have all
   // waited for it, it runs beside them and waits for their end before its own
   if (!behind_chunks) chunk::grid_wait();
-  const int first = a.queue[kLongCount] * a.H * slices;
+  // the items: the long sequences of this kernel (or all) by 32 rows, then the others by 64
+  const int from = a.queue[kLongCount], to_fine = fine_all ? a.n_seq : max(from, a.queue[kFineCount]);
+  const int per32 = a.H * (a.R / 32), per64 = a.H * (a.R / 64);
+  const int fine_items = (to_fine - from) * per32, items = fine_items + (a.n_seq - to_fine) * per64;
   const int t = threadIdx.x, lane = t & 31;
   const size_t tile = (size_t)a.R * C;
   // barriers: 1, 2 a buffer is full; 3, 4 it is empty; 5 the bringing warps among themselves;
@@ -209,21 +238,29 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs
     const bool front = t != 0 || sm >= kSmCounters || atomicAdd(a.queue + kCounters + sm, 1) == 0;
     for (;;) {
       if (t == 0) {
-        const bool any = atomicAdd(a.queue + kScanTaken, 1) < items - first;
+        const bool any = atomicAdd(a.queue + kScanTaken, 1) < items;
         s_item = !any ? items
-                      : front ? first + atomicAdd(a.queue + kScanFront, 1)
+                      : front ? atomicAdd(a.queue + kScanFront, 1)
                               : items - 1 - atomicAdd(a.queue + kScanBack, 1);
       }
       named_sync(6, kScanThreads);
       const int item = s_item;
       if (item >= items) break;
-      const int h = item % a.H, sl = item / a.H % slices;
-      const PrefillSeq q = a.seqs[item / a.H / slices];
+      const bool fine = item < fine_items;
+      const int id = fine ? item : item - fine_items, each = fine ? per32 : per64;
+      const int h = id % a.H, sl = id % each / a.H;
+      const PrefillSeq q = a.seqs[(fine ? from : to_fine) + id / each];
       if (q.dst < 0 || q.n > a.scan_most) {
         named_sync(7, kScanThreads);
         continue;
       }
       const int tiles = (q.n + kScanTok - 1) / kScanTok;
+      auto recur = [&](auto rows) {
+      constexpr int ROWS = decltype(rows)::value;
+      constexpr int RPT = ROWS / GROUPS;                // rows per thread
+      constexpr int NV = RPT * 4;                       // a thread's sums for four tokens
+      constexpr int PL = NV / LPR, LR = 4 / PL;         // the sums it keeps; lanes that hold a row's four
+      static_assert(PL == 1 || PL == 2, "sums per lane");
       const int sub = t % LPR, grp = t / LPR, lane0 = lane - sub;
       const int mine = grp + sub / LR * GROUPS, i0 = sub % LR * PL;   // the row and tokens whose sums this lane keeps
       f32x2 S[RPT][8];
@@ -249,9 +286,11 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs
           const float4 be = *reinterpret_cast<const float4 *>(K.be);
           float w[4] = {be.x * B.v[b * 4][mine], be.y * B.v[b * 4 + 1][mine], be.z * B.v[b * 4 + 2][mine],
                         be.w * B.v[b * 4 + 3][mine]};
-          float u[M2 ? 1 : NV], z[NV];   // S k_i and S q_i
+          [[maybe_unused]] float u[M2 ? 1 : NV];
+          float z[NV];   // S k_i and S q_i
           {
-            f32x2 au[M2 ? 1 : NV], az[NV];
+            [[maybe_unused]] f32x2 au[M2 ? 1 : NV];
+            f32x2 az[NV];
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
               az[j] = 0;
@@ -344,6 +383,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs
         for (int c = 0; c < 4; ++c)
           *reinterpret_cast<ulonglong2 *>(dst + c * (C / 4) + sub * 4) = make_ulonglong2(S[r][2 * c], S[r][2 * c + 1]);
       }
+      };
+      if (fine) recur(Const<32>());
+      else recur(Const<64>());
       named_sync(7, kScanThreads);   // the buffers and barriers start anew
     }
   } else {
@@ -353,25 +395,27 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs
       named_sync(6, kScanThreads);
       const int item = s_item;
       if (item >= items) break;
-      const int h = item % a.H, sl = item / a.H % slices;
-      const PrefillSeq q = a.seqs[item / a.H / slices];
+      const bool fine = item < fine_items;
+      const int id = fine ? item : item - fine_items, each = fine ? per32 : per64;
+      const int h = id % a.H, sl = id % each / a.H;
+      const PrefillSeq q = a.seqs[(fine ? from : to_fine) + id / each];
       if (q.dst < 0 || q.n > a.scan_most) {
         named_sync(7, kScanThreads);
         continue;
       }
       const int tiles = (q.n + kScanTok - 1) / kScanTok;
-      const int l = t - 128;
+      const int l = t - 128, rows = fine ? 32 : 64;
       const int hk = M2 ? h / a.hpg : h;                 // head (or group) of k and q
       const Tin *pk = static_cast<const Tin *>(a.in[1]) + (size_t)hk * C;
       const Tin *pq = static_cast<const Tin *>(a.in[M2 ? 2 : 0]) + (size_t)hk * C;
-      const Tin *pv = static_cast<const Tin *>(a.in[M2 ? 0 : 2]) + (size_t)h * a.R + sl * ROWS;
+      const Tin *pv = static_cast<const Tin *>(a.in[M2 ? 0 : 2]) + (size_t)h * a.R + sl * rows;
       const int64_t dk = a.stride[1], dq = a.stride[M2 ? 2 : 0], dv = a.stride[M2 ? 0 : 2];
       const float Ah = M2 ? __ldg(a.A + h) : 0.f;
       const float scale = M2 ? 1.f : a.out_scale;
       constexpr int per = C / 8;                         // threads per token: 16 or 8
       const int e = l / per, c8 = l % per * 8;           // this thread's token and columns
       const int bi = e & 3, bb = e & ~3;                 // its place in its block, and the block's first
-      const int ve = l / (ROWS / 4), vc = l % (ROWS / 4) * 4;   // and its four values of v
+      const int ve = fine ? l >> 3 : l >> 4, vc = (fine ? l & 7 : l & 15) * 4;   // and its four values of v
       float k8[8], q8[8], g8[8];
       // the next tile's values as they come: widened only when they are used, so that
       // nothing waits for them before
@@ -425,7 +469,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs
       auto flush = [&](int n) {   // the outputs of tile n
         const int64_t tok = (int64_t)q.tok + n * kScanTok;
         if (ve < kScanTok && ve < q.n - n * kScanTok)
-          st_stream(a.out + ((tok + ve) * a.H + h) * a.R + sl * ROWS + vc,
+          st_stream(a.out + ((tok + ve) * a.H + h) * a.R + sl * rows + vc,
                     *reinterpret_cast<const float4 *>(&buf[n & 1].o[ve][vc]));
       };
       if (tiles > 0) load(0);
@@ -557,26 +601,17 @@ __global__ void __launch_bounds__(256) requantize_kernel(const PrefillArgs a) {
   }
 }
 
-template <int KIND, typename Tin, int C, int ROWS>
-cudaError_t launch_scan_rows(const PrefillArgs &a, bool behind_chunks, cudaStream_t s) {
-  const int items = (int)((size_t)a.n_seq * a.H * (a.R / ROWS));
-  const int most = kPrefillSms * 2;
-  return launch_early(scan_kernel<KIND, Tin, C, ROWS>, (unsigned)(items < most ? items : most), kScanThreads, 0, s, a,
-                      items, behind_chunks);
-}
-
 template <int KIND, typename Tin>
 cudaError_t launch_scan(const PrefillArgs &a, bool behind_chunks, cudaStream_t s) {
-  // 32 rows per CTA while every CTA then has an SM of its own (0.18 us per token against
-  // 0.25, GDN); otherwise 64, which read the tokens half as often (32 sequences of 128
-  // tokens, 32 heads: 386 us against 584)
+  // 32 rows per item for all while every item then has an SM of its own, else for the
+  // sequences of more than kFineTokens; 64 for the others
   const bool fine = (long long)a.n_seq * a.H * a.R <= (long long)kPrefillSms * 32;
+  const size_t items = (size_t)a.n_seq * a.H * (a.R / (fine || a.scan_most > kFineTokens ? 32 : 64));
+  const unsigned grid = (unsigned)(items < 2 * kPrefillSms ? items : 2 * kPrefillSms);
   if constexpr (KIND == RSSM_MAMBA2)
     if (a.C == 64)
-      return fine ? launch_scan_rows<KIND, Tin, 64, 32>(a, behind_chunks, s)
-                  : launch_scan_rows<KIND, Tin, 64, 64>(a, behind_chunks, s);
-  return fine ? launch_scan_rows<KIND, Tin, 128, 32>(a, behind_chunks, s)
-              : launch_scan_rows<KIND, Tin, 128, 64>(a, behind_chunks, s);
+      return launch_early(scan_kernel<KIND, Tin, 64>, grid, kScanThreads, 0, s, a, (int)fine, behind_chunks);
+  return launch_early(scan_kernel<KIND, Tin, 128>, grid, kScanThreads, 0, s, a, (int)fine, behind_chunks);
 }
 
 // Sequences of up to this many tokens run four tokens at a time even where a chunked kernel

@@ -50,15 +50,26 @@ __global__ void __launch_bounds__(kPlanThreads) plan_copy_kernel(const RowsArgs 
   __syncthreads();
   const int nfree = free_slots(a.d.B, a.d.slot, a.d.freelist);
   __syncthreads();
+  // how often each row is written, and read
+  int32_t *writes = a.d.freelist + 2 * (size_t)a.d.B, *reads = writes + a.d.B;
+  for (int b = threadIdx.x; b < a.d.B; b += nt) writes[b] = reads[b] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.n; i += nt) {
+    const int d = a.dst_rows[i], s = a.src_rows[i];
+    if (d >= 0 && d < a.d.B) atomicAdd(writes + d, 1);
+    if (a.same && s >= 0 && s < a.d.B) atomicAdd(reads + s, 1);
+  }
+  __syncthreads();
   int rank = 0;
   for (int i0 = 0; i0 < a.n; i0 += nt) {
     const int i = i0 + threadIdx.x;
     Pair p;
     p.move = false;
     if (i < a.n) {
-      const int d = a.dst_rows[i];
-      const int s = a.src_rows[i];
-      p = classify(a, d, s, conflicts(a, i, d, s, 0, 1));
+      const int d = a.dst_rows[i], s = a.src_rows[i];
+      // as conflicts(): another pair writes d, or (unless d is only copied to itself) reads it
+      const bool hit = d >= 0 && d < a.d.B && (writes[d] > 1 || (a.same && d != s && reads[d] > 0));
+      p = classify(a, d, s, hit);
     }
     const bool share = p.move && a.same && p.s >= 0;
     const int need = p.move && !share;

@@ -18,8 +18,9 @@ struct PrefillSeq {
 
 // Counters in the workspace: three of the token scan's items, one of the chunked
 // kernels', the number of sequences up to the last long one, the long ones' chunks of 64
-// tokens; then CTAs begun per SM.
-enum { kScanTaken = 0, kScanFront, kScanBack, kChunkQueue, kLongCount, kChunkTotal, kCounters };
+// tokens, the number up to the last that the token scan takes by 32 rows; then CTAs begun
+// per SM.
+enum { kScanTaken = 0, kScanFront, kScanBack, kChunkQueue, kLongCount, kChunkTotal, kFineCount, kCounters };
 constexpr int kSmCounters = 256 - kCounters;
 constexpr int kPrefillSms = 148;   // CTAs of the persistent kernels, one per SM
 

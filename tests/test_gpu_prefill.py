@@ -289,3 +289,15 @@ def test_a_wait_that_runs_out_ends_the_call(kind):
     L.layer.reset()
     L.layer.ckpt.copy_(L.h0.to(DEV))
     run(L, [150, 70], [0, 1], [0, 0])
+
+
+@pytest.mark.parametrize("kind,branching", [("gdn", False), ("mamba2", True)])
+def test_more_sequences_than_planner_threads(kind, branching):
+    n = 1300
+    L = Layer(kind, batch=n + 5, heads=1, dstate=64, branching=branching)
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 5, n).tolist()
+    lens[700], lens[1200], lens[3] = 150, 70, 41
+    fresh = rng.integers(0, 2, n).tolist()
+    rows = rng.permutation(n + 5)[:n].tolist()
+    run(L, lens, rows, fresh, first=1, behind=1)
