@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
   chunk::grid_launch_next();   // the kernels behind wait for this grid themselves
   if (a.slot) adopt_folds(a.B, a.slot, a.dst, a.seen, a.flushes);
   for (int b = t; b < a.B; b += nt) a.named[b] = 0;
+  static_assert(kCounters + kSmCounters <= 256, "the smallest planner");
   if (t < kCounters + kSmCounters) a.queue[t] = 0;
   bool bad = false;
   for (int i = t; i < a.n_seq; i += nt) {
@@ -645,7 +646,7 @@ cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *
   const bool chunks = (m2_chunks || gdn_chunks) && chunked(a.kind, a.n_tokens);
   a.scan_most = chunks ? kScanMost : a.n_tokens;
   a.parts = chunks && gdn_chunks ? static_cast<uint8_t *>(work) + fixed_bytes(a.n_seq, a.B) : nullptr;
-  plan_prefill_kernel<<<1, kPlanThreads, 0, s>>>(a);
+  plan_prefill_kernel<<<1, a.n_seq > 256 || a.B > 2048 ? kPlanThreads : 256, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   ++*launches;
   if (e != cudaSuccess) return e;

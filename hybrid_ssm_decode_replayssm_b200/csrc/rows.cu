@@ -4,6 +4,7 @@
 // A row is its checkpoint (and read copy), the entries of its rings that are in
 // use, and its pointers.  Bound by HBM: each byte is read and written once.
 #include "rssm_prefill.h"
+#include "chunk.cuh"
 #include "slots.cuh"
 
 namespace rssm {
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(kMoveThreads) copy_rows_kernel(const RowsArgs 
 // front of new_row until every mover behind has read its own.
 __global__ void __launch_bounds__(kPlanThreads) plan_compact_kernel(const RowsArgs a) {
   const int B = a.d.B, nt = blockDim.x;
+  chunk::grid_launch_next();   // the moves wait for this grid themselves
   if (a.d.slot) adopt_folds(B, a.d.slot, a.d.dst, a.d.seen, a.d.flushes);
   int n_live = 0;
   for (int b0 = 0; b0 < B; b0 += nt) {
@@ -207,6 +209,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_compact_kernel(const RowsAr
 // Sources lie behind the first n_live rows and destinations among them, so no
 // row is read after it is written.
 __global__ void __launch_bounds__(kMoveThreads) compact_rows_kernel(const RowsArgs a, int nx) {
+  chunk::grid_wait();
   const int b = (int)(blockIdx.x / nx), x = (int)(blockIdx.x % nx);
   const int to = a.new_row[b];
   if (to >= 0 && to != b) move_row(a, to, b, x, nx);
@@ -238,14 +241,13 @@ cudaError_t copy_rows(const RowsArgs &a, int *launches, cudaStream_t s) {
 }
 
 cudaError_t compact_rows(const RowsArgs &a, int *launches, cudaStream_t s) {
-  plan_compact_kernel<<<1, kPlanThreads, 0, s>>>(a);
+  plan_compact_kernel<<<1, a.d.B > 256 ? kPlanThreads : 256, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   *launches = 1;
   if (e != cudaSuccess) return e;
   const int nx = parts(a, (a.d.B + 3) / 4);
-  compact_rows_kernel<<<(unsigned)((size_t)a.d.B * nx), kMoveThreads, 0, s>>>(a, nx);
   ++*launches;
-  return cudaGetLastError();
+  return launch_early(compact_rows_kernel, (unsigned)((size_t)a.d.B * nx), kMoveThreads, 0, s, a, nx);
 }
 
 }  // namespace rssm
