@@ -2,8 +2,15 @@
 // rows' checkpoints (or zero) to their new checkpoints, with every output.
 //
 //   plan_prefill_kernel   decides each sequence from the pointers (one CTA)
-//   scan_kernel           four tokens at a time, the state in registers
+//   m2_chunk_kernel, or   sequences of more than kScanMost bf16 tokens in chunks on the
+//   gdn_pre_kernel and    tensor cores (m2_prefill.cu, gdn_prefill.cu)
+//   gdn_chunk_kernel
+//   scan_kernel           the others, and KDA and fp32 inputs: four tokens at a time, the
+//                         state in registers, beside the chunked kernel
 //   requantize_kernel     the read copies of the rows written
+//
+// Each kernel's launch overlaps the one before (all but the last are programmatic): of a
+// short call's 18 us (Mamba-2, 7 turns) the GPU works 12, the host needs 17 to send it.
 #include "rssm_prefill.h"
 #include "chunk.cuh"
 #include "slots.cuh"
@@ -173,9 +180,6 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   return r;
 }
 
-template <typename T> __device__ __forceinline__ float ld_in(const void *p, int64_t i) {
-  return to_f32<T>(__ldg(static_cast<const T *>(p) + i));
-}
 // Eight consecutive elements (16-byte aligned), as they come and as fp32.
 template <typename T> struct Raw8 {
   uint4 x[sizeof(T) / 2];

@@ -2,7 +2,10 @@
 // emptied, and the live rows of a batch packed together.
 //
 // A row is its checkpoint (and read copy), the entries of its rings that are in
-// use, and its pointers.  Bound by HBM: each byte is read and written once.
+// use, and its pointers.  Bound by HBM: each byte is read and written once.  A row is cut
+// into parts so that the copies fill the GPU: 96 Mamba-2 rows with FP8 read copies
+// (1.04 GB) take 179 us, 5.8 TB/s, 89% of a plain copy's rate; 3 GDN rows (14 MB) 8.4 us, most
+// of it the launch and the host's call.
 #include "rssm_prefill.h"
 #include "chunk.cuh"
 #include "slots.cuh"

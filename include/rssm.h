@@ -395,9 +395,15 @@ int rssm_branch(rssm_handle *h, const int32_t *parent_dev, rssm_stream_t stream)
  * it.  A sequence whose row is out of range or named twice, or that continues a
  * row with a window, sets RSSM_STATUS_STATE and is skipped, its outputs and row
  * untouched; offsets that decrease or leave [0, n_tokens] skip all of them.
+ * Inputs of the sequences' tokens are finite, dt >= 0 with A < 0, gates in [0, 1]:
+ * a NaN or infinity in a token also reaches earlier outputs of its head and
+ * sequence (up to 127 tokens before it, whose products share a tile with it), never
+ * another sequence's.  Which kernel runs a sequence depends on its length and, for
+ * GDN, on whether n_tokens is above 192; nothing else of the batch changes its results.
  * The workspace (rssm_prefill_workspace_size for the same n_seq and n_tokens;
- * 256-byte aligned) holds the call's plan: it needs no initialisation and may be
- * reused by later calls on the same stream, not by calls that may run at once.
+ * 256-byte aligned) holds the call's plan and, for GDN layers with bf16 inputs, 416
+ * bytes per token and head: it needs no initialisation and may be reused by later
+ * calls on the same stream, not by calls that may run at once.
  */
 int rssm_prefill_workspace_size(rssm_handle *h, int n_seq, int n_tokens, size_t *bytes);
 int rssm_prefill(rssm_handle *h, int n_seq, int n_tokens, const int32_t *offsets_dev,
