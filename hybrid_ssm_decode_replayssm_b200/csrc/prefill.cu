@@ -626,7 +626,7 @@ cudaError_t launch_scan(const PrefillArgs &a, bool behind_chunks, cudaStream_t s
 // the chunked kernels' two launches (192 tokens in one sequence: 38 us either way).
 constexpr int kScanMost = 40, kGdnFew = 192;
 
-bool chunked(int kind, int n_tokens) { return n_tokens > (kind == RSSM_GDN ? kGdnFew : kScanMost); }
+bool chunked(int kind, int n_tokens) { return n_tokens > (kind == RSSM_MAMBA2 ? kScanMost : kGdnFew); }
 
 size_t seq_bytes(int n_seq) { return ((size_t)n_seq * sizeof(PrefillSeq) + 255) & ~(size_t)255; }
 
@@ -637,8 +637,10 @@ size_t fixed_bytes(int n_seq, int batch) {
 }  // namespace
 
 size_t prefill_work_bytes(const rssm_layer_desc &d, int n_seq, int n_tokens) {
-  const bool parts = d.kind == RSSM_GDN && d.in_dtype == RSSM_BF16 && chunked(d.kind, n_tokens);
-  return fixed_bytes(n_seq, d.batch) + (parts ? gdn_chunk_work(n_seq, n_tokens, d.nheads) : 0);
+  const bool parts = d.kind != RSSM_MAMBA2 && d.in_dtype == RSSM_BF16 && chunked(d.kind, n_tokens);
+  return fixed_bytes(n_seq, d.batch) + (!parts                   ? 0
+                                        : d.kind == RSSM_GDN ? gdn_chunk_work(n_seq, n_tokens, d.nheads)
+                                                             : kda_chunk_work(n_seq, n_tokens, d.nheads));
 }
 
 cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *launches, cudaStream_t s) {
@@ -646,16 +648,16 @@ cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *
   a.queue = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(work) + seq_bytes(a.n_seq));
   a.named = a.queue + kCounters + kSmCounters;
   *launches = 0;
-  const bool m2_chunks = m2_chunk_path(a, in_dtype), gdn_chunks = gdn_chunk_path(a, in_dtype);
-  const bool chunks = (m2_chunks || gdn_chunks) && chunked(a.kind, a.n_tokens);
+  const bool m2_chunks = m2_chunk_path(a, in_dtype), delta_chunks = gdn_chunk_path(a, in_dtype) || kda_chunk_path(a, in_dtype);
+  const bool chunks = (m2_chunks || delta_chunks) && chunked(a.kind, a.n_tokens);
   a.scan_most = chunks ? kScanMost : a.n_tokens;
-  a.parts = chunks && gdn_chunks ? static_cast<uint8_t *>(work) + fixed_bytes(a.n_seq, a.B) : nullptr;
+  a.parts = chunks && delta_chunks ? static_cast<uint8_t *>(work) + fixed_bytes(a.n_seq, a.B) : nullptr;
   plan_prefill_kernel<<<1, a.n_seq > 256 || a.B > 2048 ? kPlanThreads : 256, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   ++*launches;
   if (e != cudaSuccess) return e;
   if (chunks) {
-    e = m2_chunks ? m2_chunk_prefill(a, s) : gdn_chunk_prefill(a, s);
+    e = m2_chunks ? m2_chunk_prefill(a, s) : a.kind == RSSM_GDN ? gdn_chunk_prefill(a, s) : kda_chunk_prefill(a, s);
     *launches += m2_chunks ? 1 : 2;
     if (e != cudaSuccess) return e;
   }

@@ -66,6 +66,11 @@ bool gdn_chunk_path(const PrefillArgs &a, int in_dtype);
 size_t gdn_chunk_work(int n_seq, int n_tokens, int H);
 cudaError_t gdn_chunk_prefill(const PrefillArgs &a, cudaStream_t s);   // two kernels
 
+// The same with a gate per key channel (kda_prefill.cu): KDA, bf16 inputs.
+bool kda_chunk_path(const PrefillArgs &a, int in_dtype);
+size_t kda_chunk_work(int n_seq, int n_tokens, int H);
+cudaError_t kda_chunk_prefill(const PrefillArgs &a, cudaStream_t s);   // two kernels
+
 // Dynamic shared memory beyond the default, asked for once per kernel and device.
 inline cudaError_t allow_smem(void (*kernel)(PrefillArgs), int bytes) {
   struct Seen {
