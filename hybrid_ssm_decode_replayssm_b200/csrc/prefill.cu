@@ -623,10 +623,13 @@ cudaError_t launch_scan(const PrefillArgs &a, bool behind_chunks, cudaStream_t s
 // serves the layer, whose first chunk costs as much as a full one (32 sequences on 32 GDN
 // heads: at 32 tokens 117 us against 147, at 64 tokens 217 against 163; Mamba-2 on 128
 // heads 180 against 240 and 309 against 246).  A GDN call of few tokens in all does without
-// the chunked kernels' two launches (192 tokens in one sequence: 38 us either way).
-constexpr int kScanMost = 40, kGdnFew = 192;
+// the chunked kernels' two launches (192 tokens in one sequence: 38 us either way; KDA 51
+// against 60).  KDA's chunks cost more (32 sequences on 32 heads: at 96 tokens 333 us
+// against 364, at 128 tokens 436 against 371).
+constexpr int kScanMost = 40, kScanMostKda = 96, kDeltaFew = 192;
 
-bool chunked(int kind, int n_tokens) { return n_tokens > (kind == RSSM_MAMBA2 ? kScanMost : kGdnFew); }
+int scan_most(int kind) { return kind == RSSM_KDA ? kScanMostKda : kScanMost; }
+bool chunked(int kind, int n_tokens) { return n_tokens > (kind == RSSM_MAMBA2 ? kScanMost : kDeltaFew); }
 
 size_t seq_bytes(int n_seq) { return ((size_t)n_seq * sizeof(PrefillSeq) + 255) & ~(size_t)255; }
 
@@ -650,7 +653,7 @@ cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *
   *launches = 0;
   const bool m2_chunks = m2_chunk_path(a, in_dtype), delta_chunks = gdn_chunk_path(a, in_dtype) || kda_chunk_path(a, in_dtype);
   const bool chunks = (m2_chunks || delta_chunks) && chunked(a.kind, a.n_tokens);
-  a.scan_most = chunks ? kScanMost : a.n_tokens;
+  a.scan_most = chunks ? scan_most(a.kind) : a.n_tokens;
   a.parts = chunks && delta_chunks ? static_cast<uint8_t *>(work) + fixed_bytes(a.n_seq, a.B) : nullptr;
   plan_prefill_kernel<<<1, a.n_seq > 256 || a.B > 2048 ? kPlanThreads : 256, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
