@@ -6,13 +6,13 @@
 //   A_ts = b_t sum_c d_ts k_t k_s (s < t)      T = (I + A)^-1
 //   M_ts = scale sum_c d_ts q_t k_s (s <= t)
 //   W = T R,  R_t = b_t (v_t - S (p_t k_t))
-//   O_t = S (scale p_t q_t) + sum_{s<=t} M_ts w_s
+//   O_t = scale S (p_t q_t) + sum_{s<=t} M_ts w_s
 //   S' = S diag(p_last) + sum_s w_s (f_s k_s)^T
 // Every gate product is a product, never a ratio, so none overflows and gates of 0 hold.
 // As in the kernel of scalar gates everything that depends on the state is computed transposed,
 // one value row per tensor-memory lane; here both operands of every product are fp32 in three
 // bf16 parts, six products each:
-//   U^T = S K^T, Z^T = S Q^T (K, Q: p_t k_t, scale p_t q_t), W^T = R^T T^T, S' += W^T F
+//   U^T = S K^T, Z^T = S Q^T (K, Q: p_t k_t, p_t q_t), W^T = R^T T^T, S' += W^T F
 //   (F: f_s k_s), O^T = W^T M^T
 // T and M come from a kernel before (kda_pre_kernel), which has no chain to wait for.
 #include "delta_t.cuh"
@@ -469,10 +469,7 @@ __global__ void __launch_bounds__(kThreadsK, 1) kda_chunk_kernel(const PrefillAr
           times(p, g[0]);
           uint8_t *at = to + sw128(tg * 4 + j, (ch >> 3) & 7);
           put(at, 2 * kBlk, p, k[0]);
-          float ps[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) ps[c] = a.out_scale * p[c];
-          put(at + kPart, 2 * kBlk, ps, x[0]);
+          put(at + kPart, 2 * kBlk, p, x[0]);
           down_by_one();
           x[0] = x[1];
           x[1] = x[2];
@@ -498,7 +495,7 @@ __global__ void __launch_bounds__(kThreadsK, 1) kda_chunk_kernel(const PrefillAr
           }
 #pragma unroll
           for (int j = 0; j < 16; ++j, o += step)
-            if (c + j < left) __stcs(o, z[j] + m[j]);
+            if (c + j < left) __stcs(o, fmaf(a.out_scale, z[j], m[j]));
         }
       }
       if (i < chunks) {

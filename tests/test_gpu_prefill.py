@@ -136,6 +136,30 @@ def test_extreme_gates_and_zero_keys(kind):
         run(L, [149, 1], [1, 0], [0, 0], tol=5 * TOL, toks=toks)
 
 
+@pytest.mark.parametrize("kind", ["gdn", "kda"])
+def test_extreme_gates_in_chunks(kind):
+    """The same in sequences that run in chunks of 64 (every place in and between their blocks of
+    sixteen tokens), with channels of their own for KDA."""
+    L = Layer(kind, batch=2, heads=2)
+    toks = L.tokens(350, 19)
+    gate, b = toks[3], toks[4]
+    g = torch.Generator().manual_seed(5)
+    if kind == "kda":
+        gate[torch.rand(gate.shape, generator=g) < 0.02] = 0.0
+        gate[torch.rand(gate.shape, generator=g) < 0.02] = 1e-30
+        gate[:, :, 5] = 1.0
+    gate[[0, 15, 16, 31, 64, 80, 127, 200]] = 0.0
+    gate[[7, 47, 48, 90, 91, 128, 250]] = 1e-30
+    gate[160:190] = 1e-4
+    b[[33, 100]] = 0.0
+    b[[34, 101]] = 1.0
+    toks[1][[40, 129]] = 0.0
+    # KDA's channel 5 never forgets by its gate, only by the keys: its values stay below sqrt(350)
+    # of one token's, the errors of 350 tokens on it a factor 350 / 14 of TOL's on one of 128
+    # channels of a row, so (350 / 14) / sqrt(128) TOL on its root mean square
+    run(L, [201, 149], [1, 0], [0, 0], tol=3 * TOL, toks=toks)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_fresh_rows_do_not_read_what_was_there(kind):
     L = Layer(kind, batch=3, heads=2)
@@ -260,7 +284,7 @@ def test_many_items_of_all_lengths(kind):
         assert (after[r] == L.state[r]).all()
 
 
-@pytest.mark.parametrize("kind", ["gdn", "mamba2"])
+@pytest.mark.parametrize("kind", KINDS)
 def test_outputs_of_one_sequence_do_not_depend_on_the_others(kind):
     """A long sequence alone and in a batch gives the same bits (a short call may go by another
     kernel, so the sequence is long enough for either)."""
@@ -273,7 +297,7 @@ def test_outputs_of_one_sequence_do_not_depend_on_the_others(kind):
     assert torch.equal(one, all_[100:500]) and torch.equal(L.layer.ckpt[2], M.layer.ckpt[2])
 
 
-@pytest.mark.parametrize("kind", ["gdn", "mamba2"])
+@pytest.mark.parametrize("kind", KINDS)
 def test_a_wait_that_runs_out_ends_the_call(kind):
     """The armed self-test: a chunked kernel's wait gives up, the status says TIMEOUT, and after a
     reset the layer works again."""
