@@ -14,7 +14,10 @@ static_assert(32 * kTLd <= kFloatsX, "the blocks on the way");
 // Pairs of parts whose product matters in fp32.  Sums run from the small parts to the
 // large: the tensor core truncates each addition, and only those of the last, large
 // parts then count (1.1e-6 of the result's norm in the other order, 8192 tokens).
-__device__ constexpr int kPa[6] = {1, 0, 2, 0, 1, 0}, kPb[6] = {1, 2, 0, 1, 0, 0};
+// (1,1) (0,2) (2,0) (0,1) (1,0) (0,0), four bits each, for loops that stay rolled: code in a
+// straight line waits for its instructions (GDN, 8192 tokens on 32 heads: 701 us against 686).
+__device__ __forceinline__ uint32_t part_a(int c) { return 0x010201u >> (4 * c) & 3u; }
+__device__ __forceinline__ uint32_t part_b(int c) { return 0x001021u >> (4 * c) & 3u; }
 
 // (4 x NC outputs) sum_k L[k][r..r+3] R[k][c..c+NC-1], k < n: the left operand is stored
 // by columns, the right by rows.

@@ -18,11 +18,15 @@
 // from a kernel of its own before (gdn_pre_kernel), which has no chain to wait for.
 // Far decays are differences of double prefix sums kept as two floats.
 //
-// Bound by the chain S -> U -> R -> W -> S' of one chunk after the other.
+// Bound by the chain S -> U -> R -> W -> S' of one chunk after the other, 4.6 us a chunk on
+// one SM per head, so one sequence of 32 heads has 32 of the SMs: 8192 tokens take 690 us
+// (0.34 GB of inputs, outputs and states), of them 72 in gdn_pre_kernel; a ragged batch of
+// 11 sequences and 20011 tokens 835 us.
 //
 // Roles: warps 0-7 the chain (one value row per lane, two halves of the columns),
 // warps 8-11 and 12-15 M and the outputs of every second chunk, warp 16 issues
-// the products, warps 18-19 load the tiles with zeros behind the sequence's end.
+// the products, warps 18-19 load the tiles with zeros behind the sequence's end; warp 17
+// only fills its warpgroup.
 #include "delta_t.cuh"
 #include "rssm_prefill.h"
 
@@ -439,7 +443,6 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     // -------------------------------------------------------- the products
     fewer_registers<kRegsRest>();
     auto kmaj = [](uint32_t tile, int k) { return desc_sw128(tile + (k / 4) * kBlk + (k % 4) * 32, 16); };
-    auto mnmaj = [](uint32_t tile, int k) { return desc_sw128(tile + k * 2048, kBlk); };
     auto gram = [&](int i) {   // [K; Q] K^T
       const uint32_t kq = base + kOffKQ + (i & 1) * 2 * kBlk;
       if (elect_one()) {
@@ -453,13 +456,14 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     // S (rows of tile)^T over half of the columns: 32 from either half of the chain
     auto state_product = [&](uint32_t d, uint32_t tile, int half) {
       if (elect_one()) {
-#pragma unroll
+        const uint64_t b = desc_sw128(tile, 16);
+#pragma unroll 1
         for (int p = 2; p >= 0; --p)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int kk = (k & 1) + 4 * (k >> 1) + 2 * half;
-            mma_ts(tm + d, tm + kTmS + p * 64 + kk * 8, kmaj(tile, kk), idesc(128, kT, false, false),
-                   half > 0 || p < 2 || k > 0);
+            mma_ts(tm + d, tm + kTmS + p * 64 + kk * 8, b + ((kk / 4) * kBlk + (kk % 4) * 32) / 16,
+                   idesc(128, kT, false, false), half > 0 || p < 2 || k > 0);
           }
       }
       __syncwarp();
@@ -470,12 +474,14 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
     };
     auto pair_product = [&](uint32_t parts, uint32_t tile, uint64_t *b) {   // into U's place
       if (elect_one()) {
+        const uint64_t d = desc_sw128(tile, 16);
+#pragma unroll 1
+        for (int c = 0; c < 6; ++c) {
+          const uint32_t at = tm + parts + part_a(c) * 32;
+          const uint64_t b = d + part_b(c) * (kPart / 16);
 #pragma unroll
-        for (int c = 0; c < 6; ++c)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ts(tm + kTmU, tm + parts + kPa[c] * 32 + k * 8, desc_sw128(tile + kPb[c] * kPart + k * 32, 16),
-                   idesc(128, kT, false, false), c + k > 0);
+          for (int k = 0; k < 4; ++k) mma_ts(tm + kTmU, at + k * 8, b + k * 2, idesc(128, kT, false, false), c + k > 0);
+        }
         umma::commit(b);
       }
       __syncwarp();
@@ -514,11 +520,12 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       if (!warp_wait(bar + kFwp, ph, abort, lim)) break;
       umma::fence_after_sync();
       if (elect_one()) {
-#pragma unroll
+        const uint64_t b = desc_sw128(kq, kBlk);
+#pragma unroll 1
         for (int p = 2; p >= 0; --p)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ts(tm + kTmD, tm + kTmFw + p * 32 + k * 8, mnmaj(kq, k), idesc(128, kD, false, true), p < 2 || k > 0);
+            mma_ts(tm + kTmD, tm + kTmFw + p * 32 + k * 8, b + k * 128, idesc(128, kD, false, true), p < 2 || k > 0);
         umma::commit(bar + kUpd);
         umma::commit(bar + kStage0 + (i & 1));
       }

@@ -39,7 +39,7 @@ struct PrefillArgs {
   // workspace: the planned sequences, longest first, work counters, and a counter per row
   PrefillSeq *seqs;
   int32_t *queue;
-  uint8_t *parts;             // GDN: T of every long sequence's chunks and heads, in three bf16 parts
+  uint8_t *parts;             // GDN, KDA: what the kernel before the chunks makes of each chunk and head
   int32_t *named;
   // bookkeeping
   int32_t *len, *pending, *flushes;

@@ -228,8 +228,8 @@ int rssm_set_wait_limit(rssm_handle *h, long long cycles);
  * KDA: only the decode serving kernel (bf16 inputs) waits, so only a decode of
  * such a handle takes the path (a verify or flush launch just clears the armed
  * test); a KDA handle with fp32 inputs gives RSSM_ERR_UNSUPPORTED.
- * rssm_prefill takes the armed test too: its chunked kernels (Mamba-2 and GDN with
- * bf16 inputs, long sequences) run the path, a call without them just clears it. */
+ * rssm_prefill takes the armed test too: its chunked kernels (long sequences of
+ * bf16 inputs) run the path, a call without them just clears it. */
 int rssm_arm_timeout_test(rssm_handle *h);
 
 /*
@@ -399,11 +399,12 @@ int rssm_branch(rssm_handle *h, const int32_t *parent_dev, rssm_stream_t stream)
  * a NaN or infinity in a token also reaches earlier outputs of its head and
  * sequence (up to 127 tokens before it, whose products share a tile with it), never
  * another sequence's.  Which kernel runs a sequence depends on its length and, for
- * GDN, on whether n_tokens is above 192; nothing else of the batch changes its results.
+ * GDN and KDA, on whether n_tokens is above 192; nothing else of the batch changes its
+ * results.
  * The workspace (rssm_prefill_workspace_size for the same n_seq and n_tokens;
- * 256-byte aligned) holds the call's plan and, for GDN layers with bf16 inputs, 416
- * bytes per token and head: it needs no initialisation and may be reused by later
- * calls on the same stream, not by calls that may run at once.
+ * 256-byte aligned) holds the call's plan and, for bf16 inputs, 416 bytes per token
+ * and head of a GDN layer, 768 of a KDA layer: it needs no initialisation and may be
+ * reused by later calls on the same stream, not by calls that may run at once.
  */
 int rssm_prefill_workspace_size(rssm_handle *h, int n_seq, int n_tokens, size_t *bytes);
 int rssm_prefill(rssm_handle *h, int n_seq, int n_tokens, const int32_t *offsets_dev,
