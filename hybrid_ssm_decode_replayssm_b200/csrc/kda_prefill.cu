@@ -245,9 +245,10 @@ constexpr int kOffBar = kOffSc + (kT + 18 * kD) * 4;
 enum { kKQ = 0, kSp0, kSp1, kVf, kTf, kMf, kF, kU, kQ, kRp, kW, kWp, kUpd, kO, kOfree, kTot, kDrain, kBars };
 constexpr int kSmemK = kOffBar + kBars * 8 + 32;
 static_assert(kSmemK <= 232448, "shared memory of one CTA");
-// tensor memory columns: U^T, then W^T, then its parts 0 and 1; Z^T; the parts of S, the last of
-// them later W's part 2; the state's update, before it the parts of R; O^T
-constexpr int kTmU = 0, kTmZ = 64, kTmS = 128, kTmW2 = 256, kTmD = 320, kTmR = 320, kTmO = 448;
+// tensor memory columns: U^T, then W^T; Z^T; the parts of S; of W, in the second half of every 32
+// columns of S's (which are read by then, and written last); the state's update, before it
+// the parts of R; O^T
+constexpr int kTmU = 0, kTmZ = 64, kTmS = 128, kTmW = kTmS + 16, kTmD = 320, kTmR = 320, kTmO = 448;
 
 __global__ void __launch_bounds__(kThreadsK, 1) kda_chunk_kernel(const PrefillArgs a) {
   grid_wait();
@@ -306,6 +307,10 @@ __global__ void __launch_bounds__(kThreadsK, 1) kda_chunk_kernel(const PrefillAr
       const float *dec = s_dec + (ph ^ 1) * kD + wg * 64;
 #pragma unroll
       for (int c = 0; c < 64; c += 16) {   // the state before chunk i, and its parts
+        if (c == 32 && more && i > 0) {   // the parts of W, where these go, are read
+          good = warp_wait(bar + kO, ph ^ 1, abort, lim);
+          umma::fence_after_sync();
+        }
         if (i > 0) {
           float d[16];
           umma::ld_32x32b_x16(lanes + kTmD + wg * 64 + c, d);
@@ -328,7 +333,7 @@ __global__ void __launch_bounds__(kThreadsK, 1) kda_chunk_kernel(const PrefillAr
         }
       }
       umma::fence_before_sync();
-      if (!more) break;
+      if (!more || !good) break;
       good = warp_wait(bar + kVf, ph, abort, lim);
       if (!good) break;
       float v[32];   // v of this half's 32 tokens
@@ -362,14 +367,7 @@ __global__ void __launch_bounds__(kThreadsK, 1) kda_chunk_kernel(const PrefillAr
       umma::fence_after_sync();
       umma::ld_32x32b_x32(lanes + kTmU + wg * 32, v);
 #pragma unroll
-      for (int c = 0; c < 32; c += 16) {   // the parts of W: two in its own place, one in that of S's last
-        uint32_t hi[8], mid[8], lo[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) split3(v[c + 2 * j], v[c + 2 * j + 1], hi[j], mid[j], lo[j]);
-        st_x8(lanes + kTmU + wg * 32 + c / 2, hi);
-        st_x8(lanes + kTmU + wg * 32 + 16 + c / 2, mid);
-        st_x8(lanes + kTmW2 + wg * 16 + c / 2, lo);
-      }
+      for (int c = 0; c < 32; c += 16) split_store(lanes + kTmW + wg * 32 + c / 2, 64, v + c);
       wait_st();
       umma::fence_before_sync();
       good = warp_wait(bar + kF, ph, abort, lim);   // p_last is there; before the arrival that lets F's barrier go on
@@ -557,12 +555,11 @@ __global__ void __launch_bounds__(kThreadsK, 1) kda_chunk_kernel(const PrefillAr
       if (elect_one()) umma::commit(bar + b);
       __syncwarp();
     };
-    // pairs [from, to) of the parts of S (over half of the columns: 32 from either half of the
-    // chain) with those of K or Q
-    auto state_product = [&](uint32_t d, uint64_t tile, int half, int from, int to) {
+    // S (over half of the columns: 32 from either half of the chain) with K or Q
+    auto state_product = [&](uint32_t d, uint64_t tile, int half) {
       if (elect_one()) {
 #pragma unroll 1
-        for (int c = from; c < to; ++c) {
+        for (int c = 0; c < 6; ++c) {
           const uint32_t at = tm + kTmS + part_a(c) * 64;
           const uint64_t b = tile + part_b(c) * (2 * kBlk / 16);
 #pragma unroll
@@ -575,17 +572,6 @@ __global__ void __launch_bounds__(kThreadsK, 1) kda_chunk_kernel(const PrefillAr
       }
       __syncwarp();
     };
-    // of the parts of W: sixteen tokens k
-    // (parts 0 and 1: columns 0-15 and 16-31 of either half's 32)
-    auto w_at = [&](uint32_t p) { return tm + (p == 2 ? kTmW2 : kTmU + p * 16); };
-    auto w_step = [](uint32_t p) { return p == 2 ? 16u : 32u; };
-    auto masked = [&](int c, bool acc) {
-      const uint32_t p = part_a(c), at = w_at(p), step = w_step(p);
-      const uint64_t b = dM + part_b(c) * (kPart / 16);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        mma_ts(tm + kTmO, at + (k >> 1) * step + (k & 1) * 8, b + k * 2, idesc(128, kT, false, false), acc || k > 0);
-    };
     while (next()) {
     const int chunks = (q.n + kT - 1) / kT;
     bool good = true;
@@ -594,17 +580,17 @@ __global__ void __launch_bounds__(kThreadsK, 1) kda_chunk_kernel(const PrefillAr
       good = false;
       if (!warp_wait(bar + kKQ, ph, abort, lim)) break;
       if (!warp_wait(bar + kSp0, ph, abort, lim)) break;
-      if (i > 0 && !warp_wait(bar + kO, ph ^ 1, abort, lim)) break;   // W's parts are in U's place
       umma::fence_after_sync();
-      state_product(kTmU, dK, 0, 0, 6);
+      state_product(kTmU, dK, 0);
       if (!warp_wait(bar + kSp1, ph, abort, lim)) break;
       umma::fence_after_sync();
-      state_product(kTmU, dK, 1, 0, 6);
+      state_product(kTmU, dK, 1);
       done(kU);
       if (i > 0 && !warp_wait(bar + kOfree, ph ^ 1, abort, lim)) break;
       umma::fence_after_sync();
-      state_product(kTmZ, dQ, 0, 0, 3);   // while the chain makes R; all that reads S's last part
-      state_product(kTmZ, dQ, 1, 0, 3);
+      state_product(kTmZ, dQ, 0);   // while the chain makes R
+      state_product(kTmZ, dQ, 1);
+      done(kQ);
       if (!warp_wait(bar + kRp, ph, abort, lim) || !warp_wait(bar + kTf, ph, abort, lim)) break;
       umma::fence_after_sync();
       if (elect_one()) {
@@ -618,27 +604,31 @@ __global__ void __launch_bounds__(kThreadsK, 1) kda_chunk_kernel(const PrefillAr
         umma::commit(bar + kW);
       }
       __syncwarp();
-      state_product(kTmZ, dQ, 0, 3, 6);   // while the chain splits W
-      state_product(kTmZ, dQ, 1, 3, 6);
-      done(kQ);
-      if (!warp_wait(bar + kWp, ph, abort, lim) || !warp_wait(bar + kMf, ph, abort, lim) ||
-          !warp_wait(bar + kF, ph, abort, lim))
-        break;
+      if (!warp_wait(bar + kWp, ph, abort, lim) || !warp_wait(bar + kF, ph, abort, lim)) break;
       umma::fence_after_sync();
       if (elect_one()) {
-        masked(2, false);   // W's part 2, before the state's next parts overwrite it
 #pragma unroll 1
         for (int c = 0; c < 6; ++c) {
-          const uint32_t p = part_a(c), at = w_at(p), step = w_step(p);
+          const uint32_t at = tm + kTmW + part_a(c) * 64;
           const uint64_t b = dF + part_b(c) * (2 * kPart / 16);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ts(tm + kTmD, at + (k >> 1) * step + (k & 1) * 8, b + k * 128, idesc(128, kD, false, true), c + k > 0);
+            mma_ts(tm + kTmD, at + (k >> 1) * 32 + (k & 1) * 8, b + k * 128, idesc(128, kD, false, true), c + k > 0);
         }
         umma::commit(bar + kUpd);
+      }
+      __syncwarp();
+      if (!warp_wait(bar + kMf, ph, abort, lim)) break;
+      umma::fence_after_sync();
+      if (elect_one()) {   // the outputs, while the chain splits the next state
 #pragma unroll 1
-        for (int c = 0; c < 6; ++c)
-          if (c != 2) masked(c, true);
+        for (int c = 0; c < 6; ++c) {
+          const uint32_t at = tm + kTmW + part_a(c) * 64;
+          const uint64_t b = dM + part_b(c) * (kPart / 16);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tm + kTmO, at + (k >> 1) * 32 + (k & 1) * 8, b + k * 2, idesc(128, kT, false, false), c + k > 0);
+        }
         umma::commit(bar + kO);
       }
       __syncwarp();
