@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
 // so the sums of a row cross the lanes in two rounds instead of eight, and an element
 // costs 3.25 multiply-adds per token instead of 4.  Mamba-2: k, q, v = B, C, x,
 // no u, w = dt x.  KDA: one gate per channel, so p and d go into the vectors (p_i k_i,
-// p_i q_i, d_3j k_j).  Bound by the CUDA cores' issue and the round's latency: 0.18 us per
+// p_i q_i, d_3j k_j).  Bound by the CUDA cores' issue and the latency of those rounds: 0.18 us per
 // token of a Mamba-2 or GDN sequence, 0.22 of a KDA one, while its items have SMs of their own.
 constexpr int kScanThreads = 256;
 constexpr int kScanTok = 8;    // tokens per buffer: two blocks of four
