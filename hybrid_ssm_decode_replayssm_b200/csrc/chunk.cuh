@@ -146,6 +146,21 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// One thread tells another grid's that what its CTA wrote (before a barrier) is there.
+__device__ __forceinline__ void word_release(int32_t *p, int32_t v) {
+  asm volatile("st.release.gpu.b32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ bool word_acquire(const int32_t *p, int32_t want, long long limit) {
+  const long long t0 = clock64();
+  for (;;) {
+    int32_t v;
+    asm volatile("ld.acquire.gpu.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    if (v == want) return true;
+    if (clock64() - t0 > limit) return false;
+    __nanosleep(64);
+  }
+}
+
 // The next (sequence, head) of a persistent chunk kernel, longest sequences first: every
 // thread of the CTA calls, having finished the one before.  False: none is left, or a
 // wait gave up.

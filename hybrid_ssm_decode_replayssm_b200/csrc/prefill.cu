@@ -136,6 +136,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_prefill_kernel(const Prefil
     }
     if (t == 0) a.queue[kChunkTotal] = total;
   }
+  if (a.chunks) {   // for the scan; the armed self-test keeps it waiting
+    __syncthreads();
+    if (t == 0 && !a.stall_test) chunk::word_release(a.queue + kPlanned, kPlanWritten);
+  }
 }
 
 // -------------------------------------------------------- four tokens at a time
@@ -209,7 +213,7 @@ template <int N> struct Const {
 };
 
 template <int KIND, typename Tin, int C>
-__global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs a, int fine_all, bool behind_chunks) {
+__global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs a, int fine_all) {
   constexpr bool M2 = KIND == RSSM_MAMBA2, KDA = KIND == RSSM_KDA;
   constexpr int LPR = C / 16;                       // lanes per row
   constexpr int GROUPS = 128 / LPR;                 // rows per pass: 16 or 32
@@ -223,9 +227,21 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs
   __shared__ __align__(16) float raw_k[KDA ? kScanTok : 1][C], raw_g[KDA ? kScanTok : 1][C];
   __shared__ __align__(16) float s_gate[kScanTok], s_beta[kScanTok];
   __shared__ int s_item;
-  // alone, this grid waits for the planner's; behind a chunked kernel, whose CTAs have all
-  // waited for it, it runs beside them and waits for their end before its own
-  if (!behind_chunks) chunk::grid_wait();
+  // Alone, this grid waits for the planner's.  Beside a chunked kernel, whose CTAs have all
+  // waited for the planner before this grid began, its own wait would be for the chunked
+  // kernel's end, so that comes last; what the planner wrote is taken behind a word that it
+  // releases.  The last CTA to end takes the word back, for the next call in this workspace.
+  if (!a.chunks) {
+    chunk::grid_wait();
+  } else {
+    if (threadIdx.x == 0) s_item = chunk::word_acquire(a.queue + kPlanned, kPlanWritten, a.wait_limit);
+    __syncthreads();
+    if (!s_item) {
+      if (threadIdx.x == 0) atomicOr(a.status, (unsigned)RSSM_STATUS_TIMEOUT);
+      return chunk::grid_wait();
+    }
+    __syncthreads();
+  }
   // the items: the long sequences of this kernel (or all) by 32 rows, then the others by 64
   const int from = a.queue[kLongCount], to_fine = fine_all ? a.n_seq : max(from, a.queue[kFineCount]);
   const int per32 = a.H * (a.R / 32), per64 = a.H * (a.R / 64);
@@ -587,7 +603,10 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs
       named_sync(7, kScanThreads);
     }
   }
-  if (behind_chunks) chunk::grid_wait();
+  if (a.chunks) {
+    chunk::grid_wait();
+    if (threadIdx.x == 0 && atomicAdd(a.queue + kScanEnded, 1) == (int)gridDim.x - 1) a.queue[kPlanned] = 0;
+  }
 }
 
 // ------------------------------------------------------------- read copies
@@ -608,7 +627,7 @@ __global__ void __launch_bounds__(256) requantize_kernel(const PrefillArgs a) {
 }
 
 template <int KIND, typename Tin>
-cudaError_t launch_scan(const PrefillArgs &a, bool behind_chunks, cudaStream_t s) {
+cudaError_t launch_scan(const PrefillArgs &a, cudaStream_t s) {
   // 32 rows per item for all while every item then has an SM of its own, else for the
   // sequences of more than kFineTokens; 64 for the others
   const bool fine = (long long)a.n_seq * a.H * a.R <= (long long)kPrefillSms * 32;
@@ -616,8 +635,8 @@ cudaError_t launch_scan(const PrefillArgs &a, bool behind_chunks, cudaStream_t s
   const unsigned grid = (unsigned)(items < 2 * kPrefillSms ? items : 2 * kPrefillSms);
   if constexpr (KIND == RSSM_MAMBA2)
     if (a.C == 64)
-      return launch_early(scan_kernel<KIND, Tin, 64>, grid, kScanThreads, 0, s, a, (int)fine, behind_chunks);
-  return launch_early(scan_kernel<KIND, Tin, 128>, grid, kScanThreads, 0, s, a, (int)fine, behind_chunks);
+      return launch_early(scan_kernel<KIND, Tin, 64>, grid, kScanThreads, 0, s, a, (int)fine);
+  return launch_early(scan_kernel<KIND, Tin, 128>, grid, kScanThreads, 0, s, a, (int)fine);
 }
 
 // Sequences of up to this many tokens run four tokens at a time even where a chunked kernel
@@ -654,6 +673,7 @@ cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *
   *launches = 0;
   const bool m2_chunks = m2_chunk_path(a, in_dtype), delta_chunks = gdn_chunk_path(a, in_dtype) || kda_chunk_path(a, in_dtype);
   const bool chunks = (m2_chunks || delta_chunks) && chunked(a.kind, a.n_tokens);
+  a.chunks = chunks;
   a.scan_most = chunks ? scan_most(a.kind) : a.n_tokens;
   a.parts = chunks && delta_chunks ? static_cast<uint8_t *>(work) + fixed_bytes(a.n_seq, a.B) : nullptr;
   plan_prefill_kernel<<<1, a.n_seq > 256 || a.B > 2048 ? kPlanThreads : 256, 0, s>>>(a);
@@ -668,13 +688,13 @@ cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *
   const bool bf16 = in_dtype == RSSM_BF16;
   switch (a.kind) {
     case RSSM_MAMBA2:
-      e = bf16 ? launch_scan<RSSM_MAMBA2, __nv_bfloat16>(a, chunks, s) : launch_scan<RSSM_MAMBA2, float>(a, chunks, s);
+      e = bf16 ? launch_scan<RSSM_MAMBA2, __nv_bfloat16>(a, s) : launch_scan<RSSM_MAMBA2, float>(a, s);
       break;
     case RSSM_GDN:
-      e = bf16 ? launch_scan<RSSM_GDN, __nv_bfloat16>(a, chunks, s) : launch_scan<RSSM_GDN, float>(a, chunks, s);
+      e = bf16 ? launch_scan<RSSM_GDN, __nv_bfloat16>(a, s) : launch_scan<RSSM_GDN, float>(a, s);
       break;
     default:
-      e = bf16 ? launch_scan<RSSM_KDA, __nv_bfloat16>(a, chunks, s) : launch_scan<RSSM_KDA, float>(a, chunks, s);
+      e = bf16 ? launch_scan<RSSM_KDA, __nv_bfloat16>(a, s) : launch_scan<RSSM_KDA, float>(a, s);
   }
   ++*launches;
   if (e != cudaSuccess || read_fmt == RSSM_READ_FP32) return e;

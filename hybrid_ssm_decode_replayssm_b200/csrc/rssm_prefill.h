@@ -18,9 +18,12 @@ struct PrefillSeq {
 
 // Counters in the workspace: three of the token scan's items, one of the chunked
 // kernels', the number of sequences up to the last long one, the long ones' chunks of 64
-// tokens, the number up to the last that the token scan takes by 32 rows; then CTAs begun
+// tokens, the number up to the last that the token scan takes by 32 rows; the word that says
+// the plan is written, and the scan's CTAs that have ended (see scan_kernel); then CTAs begun
 // per SM.
-enum { kScanTaken = 0, kScanFront, kScanBack, kChunkQueue, kLongCount, kChunkTotal, kFineCount, kCounters };
+enum { kScanTaken = 0, kScanFront, kScanBack, kChunkQueue, kLongCount, kChunkTotal, kFineCount, kPlanned, kScanEnded,
+       kCounters };
+constexpr int kPlanWritten = 0x5EA7ED01;   // in kPlanned; anything else: not yet
 constexpr int kSmCounters = 256 - kCounters;
 constexpr int kPrefillSms = 148;   // CTAs of the persistent kernels, one per SM
 
@@ -29,6 +32,7 @@ struct PrefillArgs {
   int B, H, G, hpg, R, C;
   int n_seq, n_tokens;
   int scan_most;              // longest sequence of the token-by-token kernel
+  int chunks;                 // a chunked kernel runs in the call, the token scan beside it
   float out_scale;
   const float *A, *D;
   float *hc;
@@ -49,7 +53,7 @@ struct PrefillArgs {
   uint8_t *rc_codes;
   void *rc_scales;
   long long wait_limit;
-  int stall_test;             // the first CTA of a chunked kernel takes the timeout path
+  int stall_test;             // the first CTA of a chunked kernel, and the scan beside it, take the timeout path
 };
 
 // Bytes of the caller's workspace of one call.

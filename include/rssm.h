@@ -229,7 +229,8 @@ int rssm_set_wait_limit(rssm_handle *h, long long cycles);
  * such a handle takes the path (a verify or flush launch just clears the armed
  * test); a KDA handle with fp32 inputs gives RSSM_ERR_UNSUPPORTED.
  * rssm_prefill takes the armed test too: its chunked kernels (long sequences of
- * bf16 inputs) run the path, a call without them just clears it. */
+ * bf16 inputs) run the path, and the kernel of the short ones beside them waits for
+ * a plan that is not announced; a call without chunked kernels just clears it. */
 int rssm_arm_timeout_test(rssm_handle *h);
 
 /*

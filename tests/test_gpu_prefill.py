@@ -1,5 +1,7 @@
 """rssm_prefill against the token-by-token fp64 recurrences: ragged lengths, every layer
 kind and input type, strides, read copies, branching, refusals, graphs and streams."""
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
@@ -325,3 +327,58 @@ def test_more_sequences_than_planner_threads(kind, branching):
     fresh = rng.integers(0, 2, n).tolist()
     rows = rng.permutation(n + 5)[:n].tolist()
     run(L, lens, rows, fresh, first=1, behind=1)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_the_scan_beside_chunks_waits_for_the_plan(kind):
+    """Beside a chunked kernel the short sequences' kernel takes the plan only once the planner says
+    that it is written; in the armed self-test it does not, and the wait ends with TIMEOUT and
+    the short sequences' rows and outputs as they were."""
+    L = Layer(kind, batch=4, heads=2)
+    toks = [t.to(DEV) for t in L.tokens(340, 3)]
+    out = torch.full((340, 2, L.R), -77.0, device=DEV)
+    lib, off, rows = rssm.lib(), i32([0, 20, 320, 340]), i32([3, 0, 2])
+    rssm.check(lib.rssm_set_wait_limit(L.layer.handle, 2_000_000))     # about a millisecond
+    rssm.check(lib.rssm_arm_timeout_test(L.layer.handle))
+    L.layer.prefill(toks, off, out, rows=rows)
+    assert L.layer.get_status(clear=True) & rssm.RSSM_STATUS_TIMEOUT
+    assert (out[:20] == -77).all() and (out[320:] == -77).all()
+    assert (L.layer.ckpt[2:].cpu() == L.h0[2:]).all()
+    rssm.check(lib.rssm_set_wait_limit(L.layer.handle, 0))
+    L.layer.reset()
+    L.layer.ckpt.copy_(L.h0.to(DEV))
+    run(L, [20, 300, 20], [3, 0, 2], [0, 0, 0])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_one_workspace_for_many_calls(kind):
+    """Calls of other plans, one behind the other in one workspace that nobody clears: the bits of
+    calls with workspaces of their own."""
+    L, M = (Layer(kind, batch=6, heads=3) for _ in range(2))
+    plans = [([10, 300, 20, 0], [5, 0, 2, 1]), ([250, 3, 5, 120], [1, 2, 3, 0]), ([2, 200], [4, 3]),
+             ([40, 39, 38, 37, 36, 35], [0, 1, 2, 3, 4, 5]), ([1, 2, 3], [2, 1, 0])]
+    lib = rssm.lib()
+    size = C.c_size_t()
+    need = 0
+    for lens, _ in plans:
+        rssm.check(lib.rssm_prefill_workspace_size(L.layer.handle, len(lens), sum(lens), C.byref(size)))
+        need = max(need, size.value)
+    work = torch.full((need,), 0x5E, dtype=torch.uint8, device=DEV)
+    calls = []
+    for i, (lens, rows) in enumerate(plans * 4):
+        toks = [t.to(DEV) for t in L.tokens(sum(lens), i)]
+        a, b = (torch.zeros((sum(lens), 3, L.R), device=DEV) for _ in range(2))
+        calls.append((toks, i32(offsets_of(lens)), i32(rows), a, b))
+    torch.cuda.synchronize()
+    stream = torch.cuda.current_stream().cuda_stream
+    for toks, off, rows, a, _ in calls:
+        ptrs = (C.c_void_p * 5)(*[t.data_ptr() for t in toks])
+        rssm.check(lib.rssm_prefill(L.layer.handle, rows.numel(), a.shape[0], off.data_ptr(), rows.data_ptr(), None,
+                                    ptrs, None, a.data_ptr(), work.data_ptr(), need, stream))
+    for toks, off, rows, _, b in calls:
+        M.layer.prefill(toks, off, b, rows=rows)
+        torch.cuda.synchronize()
+    assert L.layer.get_status() == 0 and M.layer.get_status() == 0
+    for *_, a, b in calls:
+        assert torch.equal(a, b)
+    assert torch.equal(L.layer.ckpt, M.layer.ckpt)
