@@ -62,12 +62,15 @@ static_assert(sizeof(Scalars) % 16 == 0 && sizeof(Scalars) <= 2048, "record");
 // after the update of chunk i + 2, which the same warps' outputs precede
 constexpr int kOffBar = kOffSc + 4 * (int)sizeof(Scalars);
 enum { kFull0 = 0, kFull1, kStage0, kStage1, kA0, kA1, kM0, kM1, kO0, kO1,
-       kSp0, kSp1, kU, kQ, kRp, kW, kWp, kFwp, kUpd, kOfree, kAfree, kDrain, kBars };
+       kSp0, kSp1, kU, kRp, kW, kWp, kFwp, kUpd, kOfree, kAfree, kDrain, kBars };
 constexpr int kSmemG = kOffBar + kBars * 8 + 32;
 static_assert(kSmemG <= 232448, "shared memory of one CTA");
-// tensor memory columns.  U^T, then W^T, then the masked product; Z^T; the parts of S,
-// then of fw W; the state's update, before it the parts of R, then of W; [K; Q] K^T
-constexpr int kTmU = 0, kTmZ = 64, kTmS = 128, kTmFw = 128, kTmD = 320, kTmR = 320, kTmW = 320, kTmA = 448;
+// tensor memory columns.  U^T, then W^T, then the masked product; Z^T; the parts of S, then
+// of fw W and of W; the state's update, before it the parts of R; [K; Q] K^T.  Products in
+// flight together (the outputs' and the update) share no column that either writes: two of
+// unequal shape are ordered by a completed commit only.
+constexpr int kTmU = 0, kTmZ = 64, kTmS = 128, kTmFw = 128, kTmW = 224, kTmD = 320, kTmR = 320, kTmA = 448;
+static_assert(kTmFw + 96 <= kTmW && kTmW + 96 <= kTmD, "parts of W and of fw W outside the update's columns");
 
 // T = (I + A)^-1 of every chunk and head of the long sequences, in the three parts and the
 // place of each that the chain's kernel reads: everything that does not wait for a state.
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
   uint32_t *tm_slot = reinterpret_cast<uint32_t *>(smem + kOffBar + kBars * 8 + 8);
   Scalars *scs = reinterpret_cast<Scalars *>(smem + kOffSc);
   const uint32_t base = smem_u32(smem);
-  constexpr int count[kBars] = {64, 64, 1, 1, 1, 1, 4, 4, 1, 1, 8, 8, 1, 1, 8, 1, 8, 8, 1, 4, 2, 1};
+  constexpr int count[kBars] = {64, 64, 1, 1, 1, 1, 4, 4, 1, 1, 8, 8, 1, 8, 1, 8, 8, 1, 4, 2, 1};
   if (t == 0) {
     for (int i = 0; i < kBars; ++i) mbar_init(bar + i, count[i]);
     abort[0] = abort[1] = 0;   // the second is never set
@@ -335,7 +338,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       good = warp_wait(bar + kW, ph, abort, lim);
       if (!good) break;
       umma::fence_after_sync();
-      {   // W: first its parts, for the outputs; then those of fw W, for the state
+      {   // W: first its parts, for the outputs; then those of fw W, for the state; both where the
+          // parts of S were, which the products before W's have read
         umma::ld_32x32b_x32(lanes + kTmU + wg * 32, v);
 #pragma unroll
         for (int c = 0; c < 32; c += 16) split_store(lanes + kTmW + wg * 16 + c / 2, 32, v + c);
@@ -347,9 +351,6 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
           const float4 f = *reinterpret_cast<const float4 *>(&sc.fw[wg * 32 + j]);
           v[j] *= f.x; v[j + 1] *= f.y; v[j + 2] *= f.z; v[j + 3] *= f.w;
         }
-        good = warp_wait(bar + kQ, ph, abort, lim);   // the parts of S are read
-        if (!good) break;
-        umma::fence_after_sync();
 #pragma unroll
         for (int c = 0; c < 32; c += 16) split_store(lanes + kTmFw + wg * 16 + c / 2, 32, v + c);
       }
@@ -504,7 +505,6 @@ __global__ void __launch_bounds__(kThreadsG, 1) gdn_chunk_kernel(const PrefillAr
       done(bar + kU);
       state_product(kTmZ, kq + kPart, 0);   // while the chain makes R
       state_product(kTmZ, kq + kPart, 1);
-      done(bar + kQ);
       if (!warp_wait(bar + kRp, ph, abort, lim)) break;
       umma::fence_after_sync();
       pair_product(kTmR, base + kOffT + (i & 1) * 3 * kPart, bar + kW);
