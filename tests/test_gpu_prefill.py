@@ -382,3 +382,16 @@ def test_one_workspace_for_many_calls(kind):
     for *_, a, b in calls:
         assert torch.equal(a, b)
     assert torch.equal(L.layer.ckpt, M.layer.ckpt)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("step", [1e4, 1e9, 1e12, 1e30])
+def test_mamba2_steps_that_forget_everything(dtype, step):
+    """A huge dt (of a token without x) empties the state; the decays between the tokens behind it
+    keep their precision."""
+    L = Layer("mamba2", batch=2, heads=4, dtype=dtype)
+    toks = L.tokens(300, 23)
+    for t in (50, 128, 270):
+        toks[3][t] = step
+        toks[0][t] = 0.0
+    run(L, [200, 100], [1, 0], [0, 0], toks=toks)
