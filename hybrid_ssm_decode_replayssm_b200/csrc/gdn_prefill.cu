@@ -613,15 +613,13 @@ bool gdn_chunk_path(const PrefillArgs &a, int in_dtype) {
   return a.kind == RSSM_GDN && in_dtype == RSSM_BF16 && a.R == kD && a.C == kD;
 }
 
-size_t gdn_chunk_work(int n_seq, int n_tokens, int H) {
-  return ((size_t)n_tokens / kT + n_seq) * H * kRecord;
-}
+size_t gdn_chunk_work(size_t chunks, int H) { return chunks * H * kRecord; }
 
 cudaError_t gdn_chunk_prefill(const PrefillArgs &a, cudaStream_t s) {
   cudaError_t e = allow_smem(gdn_pre_kernel, kSmemPre);
   if (e == cudaSuccess) e = allow_smem(gdn_chunk_kernel, kSmemG);
   if (e != cudaSuccess) return e;
-  const size_t chunks = ((size_t)a.n_tokens / kT + a.n_seq) * a.H, items = (size_t)a.n_seq * a.H;
+  const size_t chunks = most_chunks(a.n_seq, a.n_tokens, a.scan_most) * a.H, items = (size_t)a.n_seq * a.H;
   e = launch_early(gdn_pre_kernel, (unsigned)(chunks < 4 * kPrefillSms ? chunks : 4 * kPrefillSms), kPreThreads, kSmemPre,
                    s, a);
   if (e != cudaSuccess) return e;

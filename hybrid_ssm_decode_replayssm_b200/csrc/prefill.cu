@@ -660,10 +660,12 @@ size_t fixed_bytes(int n_seq, int batch) {
 }  // namespace
 
 size_t prefill_work_bytes(const rssm_layer_desc &d, int n_seq, int n_tokens) {
-  const bool parts = d.kind != RSSM_MAMBA2 && d.in_dtype == RSSM_BF16 && chunked(d.kind, n_tokens);
-  return fixed_bytes(n_seq, d.batch) + (!parts                   ? 0
-                                        : d.kind == RSSM_GDN ? gdn_chunk_work(n_seq, n_tokens, d.nheads)
-                                                             : kda_chunk_work(n_seq, n_tokens, d.nheads));
+  size_t parts = 0;
+  if (d.kind != RSSM_MAMBA2 && d.in_dtype == RSSM_BF16 && chunked(d.kind, n_tokens)) {
+    const size_t chunks = most_chunks(n_seq, n_tokens, scan_most(d.kind));
+    parts = d.kind == RSSM_GDN ? gdn_chunk_work(chunks, d.nheads) : kda_chunk_work(chunks, d.nheads);
+  }
+  return fixed_bytes(n_seq, d.batch) + parts;
 }
 
 cudaError_t prefill(PrefillArgs a, void *work, int in_dtype, int read_fmt, int *launches, cudaStream_t s) {

@@ -67,13 +67,20 @@ cudaError_t m2_chunk_prefill(const PrefillArgs &a, cudaStream_t s);   // sequenc
 
 // The chunked gated delta rule (gdn_prefill.cu): GDN, bf16 inputs.
 bool gdn_chunk_path(const PrefillArgs &a, int in_dtype);
-size_t gdn_chunk_work(int n_seq, int n_tokens, int H);
+size_t gdn_chunk_work(size_t chunks, int H);   // bytes for that many chunks of 64 tokens
 cudaError_t gdn_chunk_prefill(const PrefillArgs &a, cudaStream_t s);   // two kernels
 
 // The same with a gate per key channel (kda_prefill.cu): KDA, bf16 inputs.
 bool kda_chunk_path(const PrefillArgs &a, int in_dtype);
-size_t kda_chunk_work(int n_seq, int n_tokens, int H);
+size_t kda_chunk_work(size_t chunks, int H);
 cudaError_t kda_chunk_prefill(const PrefillArgs &a, cudaStream_t s);   // two kernels
+
+// Chunks of 64 tokens that the sequences of more than scan_most tokens can have in a call: they are
+// no more than those tokens allow, however many sequences there are.
+inline size_t most_chunks(int n_seq, int n_tokens, int scan_most) {
+  const size_t fit = (size_t)n_tokens / ((size_t)scan_most + 1);
+  return (size_t)n_tokens / 64 + (fit < (size_t)n_seq ? fit : (size_t)n_seq);
+}
 
 // Dynamic shared memory beyond the default, asked for once per kernel and device.
 inline cudaError_t allow_smem(void (*kernel)(PrefillArgs), int bytes) {

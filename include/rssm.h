@@ -403,9 +403,11 @@ int rssm_branch(rssm_handle *h, const int32_t *parent_dev, rssm_stream_t stream)
  * GDN and KDA, on whether n_tokens is above 192; nothing else of the batch changes its
  * results.
  * The workspace (rssm_prefill_workspace_size for the same n_seq and n_tokens;
- * 256-byte aligned) holds the call's plan and, for bf16 inputs, 416 bytes per token
- * and head of a GDN layer, 768 of a KDA layer: it needs no initialisation and may be
- * reused by later calls on the same stream, not by calls that may run at once.
+ * 256-byte aligned) holds the call's plan (32 bytes per sequence, 4 per row of the layer,
+ * 1.5 KiB) and, for more than 192 tokens of bf16 inputs, per head 26 KiB of a GDN layer,
+ * 48 KiB of a KDA layer, for each of n_tokens / 64 + min(n_seq, n_tokens / m) chunks, m = 41
+ * (GDN) or 97 (KDA) tokens, below which a sequence needs none.  It needs no initialisation and
+ * may be reused by later calls on the same stream, not by calls that may run at once.
  */
 int rssm_prefill_workspace_size(rssm_handle *h, int n_seq, int n_tokens, size_t *bytes);
 int rssm_prefill(rssm_handle *h, int n_seq, int n_tokens, const int32_t *offsets_dev,

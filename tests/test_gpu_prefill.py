@@ -395,3 +395,23 @@ def test_mamba2_steps_that_forget_everything(dtype, step):
         toks[3][t] = step
         toks[0][t] = 0.0
     run(L, [200, 100], [1, 0], [0, 0], toks=toks)
+
+
+@pytest.mark.parametrize("kind,least", [("gdn", 41), ("kda", 97)])
+def test_the_smallest_workspace(kind, least):
+    """Sequences just long enough for chunks need the whole workspace; nothing behind it is written."""
+    lens = [least] * 7 + [1, 0, 64 * 3 + 1, least - 1]
+    L = Layer(kind, batch=len(lens), heads=3)
+    T, size, lib = sum(lens), C.c_size_t(), rssm.lib()
+    rssm.check(lib.rssm_prefill_workspace_size(L.layer.handle, len(lens), T, C.byref(size)))
+    work = torch.full((size.value + 65536,), 0x3C, dtype=torch.uint8, device=DEV)
+    toks, off = L.tokens(T, 3), offsets_of(lens)
+    dev, out, doff = [t.to(DEV) for t in toks], torch.zeros((T, 3, L.R), device=DEV), i32(off)
+    ptrs = (C.c_void_p * 5)(*[t.data_ptr() for t in dev])
+    rssm.check(lib.rssm_prefill(L.layer.handle, len(lens), T, doff.data_ptr(), None, None, ptrs, None, out.data_ptr(),
+                                work.data_ptr(), size.value, torch.cuda.current_stream().cuda_stream))
+    assert L.layer.get_status() == 0 and (work[size.value:] == 0x3C).all()
+    got, after = to64(out), L.rows()
+    for i in range(len(lens)):
+        S, o = L.ref_run(L.state[i], [t[off[i]:off[i + 1]] for t in toks])
+        assert max(scaled(got[off[i]:off[i + 1]], o), scaled(after[i], S)) <= TOL, i

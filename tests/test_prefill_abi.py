@@ -1,6 +1,7 @@
 """Host-side checks of rssm_prefill, rssm_copy_rows and rssm_compact_rows: every refusal
 returns its code before anything is enqueued (no GPU used)."""
 import ctypes as C
+import random
 
 import pytest
 import torch
@@ -63,6 +64,52 @@ def test_prefill_workspace_size():
     for bad in ((None, 1, 1), (h, 0, 1), (h, 5, 1), (h, 1, -1)):
         assert size(*bad, C.byref(n)) == rssm.RSSM_ERR_INVALID_ARG
     assert size(h, 1, 1, None) == rssm.RSSM_ERR_INVALID_ARG
+    rssm.lib().rssm_destroy(h)
+
+
+def _work_size(h, n_seq, n_tokens):
+    n = C.c_size_t()
+    assert rssm.lib().rssm_prefill_workspace_size(h, n_seq, n_tokens, C.byref(n)) == rssm.RSSM_OK
+    return n.value
+
+
+RECORD = {rssm.RSSM_GDN: (26 * 1024, 41), rssm.RSSM_KDA: (48 * 1024, 97)}   # bytes per chunk and head, shortest in chunks
+
+
+@pytest.mark.parametrize("kind", list(RECORD))
+def test_prefill_workspace_of_many_short_turns(kind):
+    """The workspace is what the header says: chunks that the tokens allow, not one per sequence."""
+    each, least = RECORD[kind]
+    h = _handle(kind, batch=256, nheads=32)
+    plan = lambda n: 32 * n + 4 * 256 + 1536   # noqa: E731
+    for n_seq, T in ((256, 256), (256, 193), (200, 400), (256, 5000), (3, 5000), (1, 8192)):
+        got = _work_size(h, n_seq, T)
+        chunks = T // 64 + min(n_seq, T // least)
+        assert each * 32 * chunks < got <= each * 32 * chunks + plan(n_seq), (n_seq, T)
+    assert _work_size(h, 256, 192) <= plan(256)
+    rssm.lib().rssm_destroy(h)
+    for kw in (dict(kind=kind, in_dtype=rssm.RSSM_F32), dict(kind=rssm.RSSM_MAMBA2)):
+        h = _handle(batch=256, nheads=32, **kw)
+        assert _work_size(h, 256, 100000) <= plan(256)
+        rssm.lib().rssm_destroy(h)
+
+
+@pytest.mark.parametrize("kind", list(RECORD))
+def test_prefill_workspace_holds_every_batch(kind):
+    """Whatever the lengths: the chunks of the long sequences fit."""
+    each, least = RECORD[kind]
+    h = _handle(kind, batch=64, nheads=1)
+    r = random.Random(3)
+    for case in range(400):
+        n = r.randrange(1, 65)
+        top = r.choice((least, least + 1, 2 * least, 64 * 3 + 1, 700))
+        lens = [r.choice((0, 1, least - 1, least, 65, 129, r.randrange(top + 1))) for _ in range(n)]
+        if case % 4 == 0:
+            lens = [least] * n
+        T = sum(lens)
+        if T > 192:
+            used = sum(-(-x // 64) for x in lens if x >= least)
+            assert used * each <= _work_size(h, n, T) - (32 * n + 4 * 64 + 1024), (lens,)
     rssm.lib().rssm_destroy(h)
 
 
