@@ -195,11 +195,21 @@ rssm::StepArgs step_args(const rssm_handle *h, int mode, int m) {
 
 int n_inputs(const rssm_handle *h) { return h->d.kind == RSSM_MAMBA2 ? 4 : 5; }
 
-int check_inputs(const rssm_handle *h, const void *const *in, const void *out) {
+// Input i has one value per head (dt; alpha, beta), and the bytes of an element of it.
+bool per_head(const rssm_handle *h, int i) {
+  return h->d.kind == RSSM_MAMBA2 ? i == 3 : i == 4 || (i == 3 && h->d.kind == RSSM_GDN);
+}
+int input_size(const rssm_handle *h, int i) {
+  return (h->d.kind != RSSM_MAMBA2 && i >= 3) || h->d.in_dtype == RSSM_F32 ? 4 : 2;
+}
+
+// tokens: inputs of rssm_prefill, which loads those of one value per head one by one.
+int check_inputs(const rssm_handle *h, const void *const *in, const void *out, bool tokens = false) {
   if (!in) return fail(RSSM_ERR_INVALID_ARG, "in is NULL");
   for (int i = 0; i < n_inputs(h); ++i) {
     if (!in[i]) return fail(RSSM_ERR_INVALID_ARG, "in[%d] is NULL", i);
-    if (!aligned(in[i], 16)) return fail(RSSM_ERR_INVALID_ARG, "in[%d] is not 16-byte aligned", i);
+    const int to = tokens && per_head(h, i) ? input_size(h, i) : 16;
+    if (!aligned(in[i], to)) return fail(RSSM_ERR_INVALID_ARG, "in[%d] is not %d-byte aligned", i, to);
   }
   if (!out) return fail(RSSM_ERR_INVALID_ARG, "out is NULL");
   if (!aligned(out, 16)) return fail(RSSM_ERR_INVALID_ARG, "out is not 16-byte aligned");
@@ -582,7 +592,7 @@ int rssm_prefill(rssm_handle *h, int n_seq, int n_tokens, const int32_t *offsets
   if (n_tokens < 0) return fail(RSSM_ERR_INVALID_ARG, "n_tokens must be >= 0");
   if (!offsets_dev) return fail(RSSM_ERR_INVALID_ARG, "offsets is NULL");
   if (n_tokens > 0) {
-    int rc = check_inputs(h, in, out_dev);
+    int rc = check_inputs(h, in, out_dev, true);
     if (rc) return rc;
     if (!aligned(out_dev, 32)) return fail(RSSM_ERR_INVALID_ARG, "out is not 32-byte aligned");
   } else if (d.kind == RSSM_MAMBA2 && (!h->A || !h->D)) {
@@ -605,17 +615,14 @@ int rssm_prefill(rssm_handle *h, int n_seq, int n_tokens, const int32_t *offsets
   const int64_t heads = d.nheads, R = d.headdim, C = d.dstate;
   const int64_t m2[5] = {heads * R, (int64_t)d.ngroups * C, (int64_t)d.ngroups * C, heads, 0};
   const int64_t dr[5] = {heads * C, heads * C, heads * R, d.kind == RSSM_KDA ? heads * C : heads, heads};
-  const int esz = d.in_dtype == RSSM_BF16 ? 2 : 4;
   for (int i = 0; i < n_inputs(h); ++i) {
     const int64_t packed = d.kind == RSSM_MAMBA2 ? m2[i] : dr[i];
-    const bool scalar = d.kind == RSSM_MAMBA2 ? i == 3 : i == 4 || (i == 3 && d.kind == RSSM_GDN);
-    const int size = d.kind != RSSM_MAMBA2 && i >= 3 ? 4 : esz;
     a.stride[i] = in_strides ? in_strides[i] : packed;
     a.in[i] = n_tokens > 0 ? in[i] : nullptr;
     if (a.stride[i] < packed)
       return fail(RSSM_ERR_INVALID_ARG, "in_strides[%d] = %lld is less than a token's %lld elements", i,
                   (long long)a.stride[i], (long long)packed);
-    if (!scalar && a.stride[i] * size % 16)
+    if (!per_head(h, i) && a.stride[i] * input_size(h, i) % 16)
       return fail(RSSM_ERR_INVALID_ARG, "in_strides[%d]: tokens must be a multiple of 16 bytes apart", i);
   }
   a.out = static_cast<float *>(out_dev);

@@ -385,8 +385,8 @@ int rssm_branch(rssm_handle *h, const int32_t *parent_dev, rssm_stream_t stream)
  *   in[]: as rssm_decode_step with a token axis in place of the batch axis
  *   ([n_tokens, H, P], ...), 16-byte aligned.  in_strides: host array, elements
  *   from one token to the next per input (slices of a wider projection); at
- *   least a token's elements, and a multiple of 16 bytes except for the inputs
- *   with one value per head; NULL = packed.
+ *   least a token's elements, and a multiple of 16 bytes; NULL = packed.  Inputs
+ *   with one value per head (dt; GDN's alpha; beta) need neither: any element will do.
  *   out_dev: fp32 [n_tokens, H, P] / [n_tokens, H, dv], packed, 32-byte aligned.
  *   n_tokens = 0: in and out are not used and may be NULL.
  * Afterwards the row's window is empty, its read copy is rebuilt, and the call

@@ -415,3 +415,20 @@ def test_the_smallest_workspace(kind, least):
     for i in range(len(lens)):
         S, o = L.ref_run(L.state[i], [t[off[i]:off[i + 1]] for t in toks])
         assert max(scaled(got[off[i]:off[i + 1]], o), scaled(after[i], S)) <= TOL, i
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_slices_of_a_longer_run_of_tokens(kind, dtype):
+    """Inputs that begin at an odd token of a longer tensor (on a layer of three heads their dt,
+    alpha and beta are on no 16 bytes) give the bits of copies of their own, in the scan and in chunks."""
+    for T in (60, 330):
+        L, M = (Layer(kind, batch=3, heads=3, dtype=dtype) for _ in range(2))
+        long = [t.to(DEV) for t in L.tokens(T + 5, 3)]
+        part = [t[5:] for t in long]
+        assert any(t.data_ptr() % 16 for t in part)
+        outs = [torch.zeros((T, 3, L.R), device=DEV) for _ in range(2)]
+        off = i32([0, T // 2 + 1, T])
+        L.layer.prefill(part, off, outs[0])
+        M.layer.prefill([t.clone() for t in part], off, outs[1])
+        assert torch.equal(*outs) and torch.equal(L.layer.ckpt, M.layer.ckpt)

@@ -47,6 +47,24 @@ def test_prefill_arguments(kw):
     rssm.lib().rssm_destroy(h)
 
 
+@pytest.mark.parametrize("kind,dtype,free", [
+    (rssm.RSSM_MAMBA2, rssm.RSSM_BF16, {3: 2}), (rssm.RSSM_MAMBA2, rssm.RSSM_F32, {3: 4}),
+    (rssm.RSSM_GDN, rssm.RSSM_BF16, {3: 4, 4: 4}), (rssm.RSSM_KDA, rssm.RSSM_BF16, {4: 4})])
+def test_prefill_alignment_of_each_input(kind, dtype, free):
+    """Inputs with one value per head may begin at any element, the others on 16 bytes.  (The calls
+    that pass this check fail at the next, the workspace's size.)"""
+    h = _handle(kind, in_dtype=dtype)
+    for i in range(4 if kind == rssm.RSSM_MAMBA2 else 5):
+        for off in (1, 2, 4, 8):
+            ins = [FAKE] * 5
+            ins[i] += off
+            assert _prefill(h, ins=ins, nbytes=0) == rssm.RSSM_ERR_INVALID_ARG
+            text = rssm.lib().rssm_last_error_string().decode()
+            taken = i in free and off % free[i] == 0
+            assert ("workspace" if taken else f"in[{i}]") in text, (i, off, text)
+    rssm.lib().rssm_destroy(h)
+
+
 def test_prefill_needs_a_handle_and_parameters():
     assert _prefill(None) == rssm.RSSM_ERR_INVALID_ARG
     h = _handle(rssm.RSSM_MAMBA2, params=False)
