@@ -432,3 +432,113 @@ def test_slices_of_a_longer_run_of_tokens(kind, dtype):
         L.layer.prefill(part, off, outs[0])
         M.layer.prefill([t.clone() for t in part], off, outs[1])
         assert torch.equal(*outs) and torch.equal(L.layer.ckpt, M.layer.ckpt)
+
+
+# ---------------------------------------------- forms of the chunked kernels
+# A call of more than 192 tokens runs a layer's sequences of more than 96 tokens in chunks, whatever
+# its kind.  The launches tell: plan, (GDN, KDA: T of every chunk,) chunks, scan, (read copies).
+CHUNK_LAUNCHES = {"mamba2": 3, "gdn": 4, "kda": 4}
+
+
+def launches_of(call):
+    before = rssm.lib().rssm_launch_count()
+    call()
+    return rssm.lib().rssm_launch_count() - before
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_token_strides_in_chunks(kind):
+    L, M = (Layer(kind, batch=3, heads=4) for _ in range(2))
+    T = 360
+    toks = [t.to(DEV) for t in L.tokens(T, 3)]
+    wide = []
+    for i, t in enumerate(toks):
+        w = torch.full((T, t[0].numel() + 16 * (i + 1)), float("nan"), dtype=t.dtype, device=DEV)
+        at = 8 * (i + 1) if t.dtype == torch.bfloat16 else 4 * (i + 1)
+        w[:, at:at + t[0].numel()] = t.reshape(T, -1)
+        wide.append(w[:, at:at + t[0].numel()].unflatten(1, t.shape[1:]) if t.dim() == 3 else w[:, at:at + t.shape[1]])
+    outs = [torch.zeros((T, L.H, L.R), device=DEV) for _ in range(2)]
+    off = i32([0, 201, 350, T])
+    L.layer.prefill(toks, off, outs[0])
+    n = launches_of(lambda: M.layer.prefill(wide, off, outs[1]))
+    assert n == CHUNK_LAUNCHES[kind]
+    assert torch.equal(outs[0], outs[1]) and torch.equal(L.layer.ckpt, M.layer.ckpt)
+    S, o = L.ref_run(L.state[0], [t[:201].cpu() for t in toks])
+    assert scaled(to64(outs[1][:201]), o) <= TOL and scaled(M.rows()[0], S) <= TOL
+
+
+@pytest.mark.parametrize("branching", [False, True])
+@pytest.mark.parametrize("fmt", [rssm.RSSM_READ_FP8_E4M3_ROW, rssm.RSSM_READ_NVFP4])
+@pytest.mark.parametrize("kind", KINDS)
+def test_read_copies_behind_chunks(kind, fmt, branching):
+    for dstate in (64, 128) if kind == "mamba2" else (128,):
+        L = Layer(kind, batch=5, heads=2, dstate=dstate, read_fmt=fmt, branching=branching)
+        L.layer.quantize_read_copy()
+        n = launches_of(lambda: run(L, [140, 0, 201, 7], [3, 0, 1, 4], [0, 1, 1, 0]))
+        assert n >= CHUNK_LAUNCHES[kind] + 1
+        codes, scales = (t.clone() for t in L.layer.read_copy_views())
+        slots = L.layer.get_slots().tolist() if branching else list(range(5))
+        assert int(codes[slots[0]].max()) == 0            # the emptied row
+        L.layer.quantize_read_copy()
+        for got, want in zip((codes, scales), L.layer.read_copy_views()):
+            for r in slots:
+                assert torch.equal(got[r], want[r])
+        if fmt == rssm.RSSM_READ_FP8_E4M3_ROW:
+            want, _ = codecs.fp8_row_quantize(L.layer.ckpt.cpu().numpy()[slots[1], 0])
+            assert (codes[slots[1], 0].cpu().numpy() == want).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_fresh_rows_in_chunks_do_not_read_what_was_there(kind):
+    L = Layer(kind, batch=4, heads=2)
+    L.layer.ckpt[1] = float("nan")
+    L.layer.ckpt[3] = float("inf")
+    L.state[1] = L.state[3] = 0
+    run(L, [130, 5, 200], [1, 2, 3], [1, 0, 1])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_branching_rows_that_share_a_state_in_chunks(kind):
+    L = Layer(kind, batch=4, heads=2, branching=True)
+    run(L, [233], [0], [1])
+    L.layer.branch(i32([0, 0, 0, 3]))
+    L.state[1] = L.state[2] = L.state[0]
+    run(L, [120, 150], [1, 3], [0, 0], seed=7)            # row 1 goes on, rows 0 and 2 keep the prefix
+    run(L, [100, 99, 20, 130], [2, 1, 0, 3], [0, 1, 0, 0], seed=8)
+    assert len(set(L.layer.get_slots().cpu().tolist())) == 4
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_captured_chunks(kind):
+    """A captured call whose offsets then move across the lengths at which a sequence changes its
+    kernel (40 and 96 tokens): the eager results, call after call, also when it is replayed at once
+    behind itself and the eager calls stand on another stream."""
+    L, M = (Layer(kind, batch=4, heads=2) for _ in range(2))
+    T = 400
+    toks = [t.to(DEV) for t in L.tokens(T, 3)]
+    off, rows = i32([0, 201, 360, T]), i32([2, 0, 3])
+    outs = [torch.zeros((T, L.H, L.R), device=DEV) for _ in range(2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    L.layer.prefill(toks, off, outs[0], rows=rows, stream=side)
+    side.synchronize()
+    M.layer.prefill(toks, off, outs[1], rows=rows)
+    assert torch.equal(*outs) and torch.equal(L.layer.ckpt, M.layer.ckpt)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        n = launches_of(lambda: L.layer.prefill(toks, off, outs[0], rows=rows))
+    assert n == CHUNK_LAUNCHES[kind]
+    for seed, at in enumerate([(0, 40, 80, T), (0, 41, 82, 179), (0, 96, 192, 390), (10, 107, 204, 300), (0, 1, 1, T),
+                               (0, 300, 350, 380), (0, 30, 60, 90)]):
+        for t, new in zip(toks, L.tokens(T, 30 + seed)):
+            t.copy_(new)
+        off.copy_(i32(list(at)))
+        torch.cuda.synchronize()
+        graph.replay()
+        graph.replay()
+        with torch.cuda.stream(side):
+            for _ in range(2):
+                M.layer.prefill(toks, off, outs[1], rows=rows)
+        torch.cuda.synchronize()
+        assert torch.equal(*outs) and torch.equal(L.layer.ckpt, M.layer.ckpt), at
+    assert L.layer.get_status() == 0 and M.layer.get_status() == 0
