@@ -27,7 +27,13 @@ namespace {
 // Accepted sequences are listed longest first, so that the longest start first.
 constexpr int kPlanThreads = 1024;
 
-constexpr int kFineTokens = 512;   // of a sequence, above which the token scan takes it by 32 rows
+// The token scan takes sequences of more tokens than this by 32 rows per item, the others by 64,
+// as long as each of those items has an SM of its own: a shorter chain per token (fp32 inputs, 32
+// heads, one sequence of 1024 tokens beside 11 of 64: GDN 247 us against 309, KDA 319 against
+// 338), but half as many rows per reading of the tokens.  Where they are too many for that, all go
+// by 64 (4 sequences of 1024: GDN 452 us against 694 by 32, KDA 510 against 861, Mamba-2 on 128
+// heads 681 against 921); at 512 tokens beside short ones both cost the same (KDA 196, 198).
+constexpr int kFineTokens = 512;
 constexpr int kBins = 66;
 __device__ __forceinline__ int length_bin(int n, int scan_most) { return (n > scan_most ? 33 : 0) + 32 - __clz(n); }
 
@@ -243,8 +249,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs
     __syncthreads();
   }
   // the items: the long sequences of this kernel (or all) by 32 rows, then the others by 64
-  const int from = a.queue[kLongCount], to_fine = fine_all ? a.n_seq : max(from, a.queue[kFineCount]);
+  const int from = a.queue[kLongCount], to_long = max(from, a.queue[kFineCount]);
   const int per32 = a.H * (a.R / 32), per64 = a.H * (a.R / 64);
+  const int to_fine = fine_all ? a.n_seq : (long long)(to_long - from) * per32 <= kPrefillSms ? to_long : from;
   const int fine_items = (to_fine - from) * per32, items = fine_items + (a.n_seq - to_fine) * per64;
   const int t = threadIdx.x, lane = t & 31;
   const size_t tile = (size_t)a.R * C;
@@ -628,8 +635,9 @@ __global__ void __launch_bounds__(256) requantize_kernel(const PrefillArgs a) {
 
 template <int KIND, typename Tin>
 cudaError_t launch_scan(const PrefillArgs &a, cudaStream_t s) {
-  // 32 rows per item for all while every item then has an SM of its own, else for the
-  // sequences of more than kFineTokens; 64 for the others
+  // 32 rows per item for all while every item then has an SM of its own (GDN, 32 heads, fp32: 40
+  // tokens 20.5 us against 24, 1000 tokens 201 against 256; Mamba-2, 64 heads: 200 tokens 45
+  // against 51), else for a few sequences of more than kFineTokens; 64 for the others
   const bool fine = (long long)a.n_seq * a.H * a.R <= (long long)kPrefillSms * 32;
   const size_t items = (size_t)a.n_seq * a.H * (a.R / (fine || a.scan_most > kFineTokens ? 32 : 64));
   const unsigned grid = (unsigned)(items < 2 * kPrefillSms ? items : 2 * kPrefillSms);

@@ -542,3 +542,26 @@ def test_captured_chunks(kind):
         torch.cuda.synchronize()
         assert torch.equal(*outs) and torch.equal(L.layer.ckpt, M.layer.ckpt), at
     assert L.layer.get_status() == 0 and M.layer.get_status() == 0
+
+
+@pytest.mark.parametrize("heads", [8, 24])
+@pytest.mark.parametrize("kind", KINDS)
+def test_long_fp32_prompts_beside_short_ones(kind, heads):
+    """fp32 prompts of more than 512 tokens in a batch (by half as many state rows per CTA as the
+    others while they are few): the values, and the bits that each has alone in a call."""
+    lens = [600, 30, 520, 1, 0, 512, 513, 64, 5, 40, 41, 3]
+    L, M = (Layer(kind, batch=len(lens), heads=heads, dtype="f32") for _ in range(2))
+    off, toks = offsets_of(lens), L.tokens(sum(lens), 5)
+    dev = [t.to(DEV) for t in toks]
+    out = torch.zeros((off[-1], heads, L.R), device=DEV)
+    L.layer.prefill(dev, i32(off), out)
+    assert L.layer.get_status() == 0
+    got, after = to64(out), L.rows()
+    for i, n in enumerate(lens):
+        at = slice(off[i], off[i + 1])
+        one = torch.zeros((n, heads, L.R), device=DEV)
+        M.layer.prefill([t[at].clone() for t in dev], i32([0, n]), one, rows=i32([i]))
+        assert torch.equal(one, out[at]) and torch.equal(M.layer.ckpt[i], L.layer.ckpt[i]), n
+        if i in (0, 1, 6):
+            S, o = L.ref_run(L.state[i], [t[at] for t in toks])
+            assert max(scaled(got[at], o), scaled(after[i], S)) <= TOL, n
