@@ -565,3 +565,44 @@ def test_long_fp32_prompts_beside_short_ones(kind, heads):
         if i in (0, 1, 6):
             S, o = L.ref_run(L.state[i], [t[at] for t in toks])
             assert max(scaled(got[at], o), scaled(after[i], S)) <= TOL, n
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_two_layers_on_two_streams(kind):
+    """Calls of two layers at once, short and long, give the bits of the same calls in turn."""
+    Ls = [[Layer(kind, batch=3, heads=24, seed=s) for s in (1, 2)] for _ in range(2)]
+    toks = [[t.to(DEV) for t in Ls[0][0].tokens(500, 40 + s)] for s in range(2)]
+    offs = [i32([0, 300, 330, 500]), i32([0, 20, 480, 500])]
+    outs = [[torch.zeros((500, 24, Ls[0][0].R), device=DEV) for _ in range(2)] for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s in range(2):
+            Ls[0][s].layer.prefill(toks[s], offs[s], outs[0][s], stream=streams[s])
+    torch.cuda.synchronize()
+    for s in range(2):
+        for _ in range(5):
+            Ls[1][s].layer.prefill(toks[s], offs[s], outs[1][s])
+            torch.cuda.synchronize()
+        assert torch.equal(outs[0][s], outs[1][s]) and torch.equal(Ls[0][s].layer.ckpt, Ls[1][s].layer.ckpt)
+        assert Ls[0][s].layer.get_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_tokens_past_31_bits(kind, dtype):
+    """Sequences behind a place that 31 bits of elements do not reach (nothing before it is read)."""
+    L, M = (Layer(kind, batch=3, heads=64, groups=2, dtype=dtype) for _ in range(2))
+    first = (1 << 31) // (64 * L.R) + 1000
+    T = first + 260
+    if torch.cuda.mem_get_info()[0] < 80e9:
+        pytest.skip("needs 80 GB")
+    part = [t.to(DEV) for t in L.tokens(260, 3)]
+    far = [torch.empty((T,) + t.shape[1:], dtype=t.dtype, device=DEV) for t in part]
+    for f, t in zip(far, part):
+        f[first:] = t
+    out, want = (torch.zeros((n, 64, L.R), device=DEV) for n in (T, 260))
+    L.layer.prefill(far, i32([first, first + 150, first + 170, T]), out)
+    M.layer.prefill(part, i32([0, 150, 170, 260]), want)
+    assert L.layer.get_status() == 0 and torch.equal(L.layer.ckpt, M.layer.ckpt)
+    assert torch.equal(out[first:], want) and int(torch.count_nonzero(out[first - 100:first])) == 0
