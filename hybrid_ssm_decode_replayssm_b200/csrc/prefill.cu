@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_kernel(const PrefillArgs
   // the items: the long sequences of this kernel (or all) by 32 rows, then the others by 64
   const int from = a.queue[kLongCount], to_long = max(from, a.queue[kFineCount]);
   const int per32 = a.H * (a.R / 32), per64 = a.H * (a.R / 64);
-  const int to_fine = fine_all ? a.n_seq : (long long)(to_long - from) * per32 <= kPrefillSms ? to_long : from;
+  const int to_fine = fine_all ? a.n_seq : to_long - from <= kPrefillSms / per32 ? to_long : from;
   const int fine_items = (to_fine - from) * per32, items = fine_items + (a.n_seq - to_fine) * per64;
   const int t = threadIdx.x, lane = t & 31;
   const size_t tile = (size_t)a.R * C;
