@@ -375,6 +375,9 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
     while (next()) {
     const int chunks = (q.n + kT - 1) / kT;
     const double Ah = (double)__ldg(a.A + h) * 1.4426950408889634;   // in powers of two
+    // a step that forgets all: any power of two this far down does, and the sums behind it keep
+    // their precision (unbounded, a dt of 1e12 cost the decays of its chunk 1%)
+    const float most = (float)(16384.0 / fabs(Ah));
     const __nv_bfloat16 *pdt = static_cast<const __nv_bfloat16 *>(a.in[3]) + h;
     auto load = [&](int i, float (&v)[4]) {
 #pragma unroll
@@ -391,9 +394,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) m2_chunk_kernel(const PrefillArg
       double G[4], sum = 0.0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        // a step that forgets all: any power of two this far down does, and the sums behind it
-        // keep their precision (unbounded, a dt of 1e12 cost the decays of its chunk 1%)
-        sum += fmax((double)dt[k] * Ah, -16384.0);
+        sum += (double)fminf(dt[k], most) * Ah;
         G[k] = sum;
       }
       double inc = sum;
