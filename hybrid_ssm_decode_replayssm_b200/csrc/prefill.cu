@@ -9,7 +9,8 @@
 //                         registers, beside the chunked kernel
 //   requantize_kernel     the read copies of the rows written
 //
-// Each kernel's launch overlaps the one before (all but the last are programmatic): of a
+// The planner waits for all work before it, the read copies for all of the call; the kernels
+// between are launched programmatically, each resident before the one ahead of it ends.  Of a
 // short call's 18 us (Mamba-2, 7 turns) the GPU works 12, the host needs 17 to send it.
 #include "rssm_prefill.h"
 #include "chunk.cuh"
