@@ -19,9 +19,10 @@
 // Far decays are differences of double prefix sums kept as two floats.
 //
 // Bound by the chain S -> U -> R -> W -> S' of one chunk after the other, 4.6 us or 8800 cycles
-// a chunk (the tensor cores busy for 47% of them, the issue slots for 46%) on one SM per head, so one sequence of 32 heads has 32 of the SMs: 8192 tokens take 690 us
-// (0.34 GB of inputs, outputs and states), of them 72 in gdn_pre_kernel; a ragged batch of
-// 11 sequences and 20011 tokens 835 us.
+// a chunk (the tensor cores busy for 47% of them, the issue slots for 46%) on one SM per head,
+// so one sequence of 32 heads has 32 of the SMs: 8192 tokens take 690 us (0.34 GB of inputs,
+// outputs and states), of them 72 in gdn_pre_kernel; a ragged batch of 11 sequences and 20011
+// tokens 840 us.
 //
 // Roles: warps 0-7 the chain (one value row per lane, two halves of the columns),
 // warps 8-11 and 12-15 M and the outputs of every second chunk, warp 16 issues

@@ -17,11 +17,11 @@
 // T and M come from a kernel before (kda_pre_kernel), which has no chain to wait for.
 //
 // Bound by the chain S -> U -> R -> W -> S' of one chunk after the other, 12800 cycles a chunk
-// (of them 6200 the tensor core's, by its counter), and before it by the instructions of kda_pre_kernel, 12 us
-// per SM for a chunk and head.  8192 tokens on 32 heads: 1260 us, of them 350 in
-// kda_pre_kernel (0.45 GB of inputs, outputs and states); four tokens at a time on the
-// CUDA cores 1800; 8 sequences of 1024 tokens 602 against 1440.  The products unrolled take
-// 14500 cycles a chunk: their instructions are waited for.
+// (of them 6200 the tensor core's, by its counter), and before it by the instructions of
+// kda_pre_kernel, 12 us per SM for a chunk and head.  8192 tokens on 32 heads: 1265 us, of them
+// 350 in kda_pre_kernel (0.45 GB of inputs, outputs and states); four tokens at a time on the
+// CUDA cores 1800; 8 sequences of 1024 tokens 602 against 1440.  The products unrolled take 10%
+// more cycles a chunk: their instructions are waited for.
 #include "delta_t.cuh"
 #include "rssm_prefill.h"
 

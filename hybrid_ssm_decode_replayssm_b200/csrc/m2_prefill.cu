@@ -27,9 +27,9 @@
 //
 // Bound by the hand-overs from role to role in a chunk's 8200 cycles: shared memory is busy for
 // 65% of them (the kernel's loads and stores 3160, the products' operand reads 2180), the issue
-// slots for 45%, the tensor cores for 35% (counters, 3000 tokens).  8192 tokens on 128 heads (N = 128) take 280 us, 440 MB of
-// inputs, outputs and states at 1.6 TB/s; L on 16 warps of eight columns 299, L and C in
-// shared memory and y stored a token per lane slower still.
+// slots for 45%, the tensor cores for 35% (counters, 3000 tokens).  8192 tokens on 128 heads
+// (N = 128) take 280 us, 440 MB of inputs, outputs and states at 1.6 TB/s; L on 16 warps of
+// eight columns 299, L and C in shared memory and y stored a token per lane slower still.
 #include "chunk.cuh"
 #include "rssm_prefill.h"
 
